@@ -39,7 +39,7 @@
  *    no state between calls; all calls except mb_plan_status only enqueue
  *    work on `stream` and return without waiting. Calls on different streams
  *    with disjoint buffers may run concurrently. Since they neither allocate
- *    nor synchronise, mb_plan*, mb_dispatch and mb_combine* can be captured
+ *    nor synchronise, every call but mb_plan_status can be captured
  *    in a HIP graph and replayed (a drift state then advances per replay).
  *  - All integers are int32, all arrays row-major and densely packed.
  *  - Host-detectable errors (bad sizes, null pointers, misaligned rows, a
@@ -57,7 +57,7 @@
  *
  * Limits: 1 <= P <= 64, E % P == 0, E <= 1024, 1 <= K <= min(E, 32),
  * 0 <= R <= 16, N % P == 0, N*K < 2^31, P*cap < 2^31, row bytes a multiple
- * of 16; fp8 rows need H % 128 == 0. rep_expert may be NULL when R == 0.
+ * of 16; fp8 and 4-bit rows need H % 128 == 0. rep_expert may be NULL when R == 0.
  */
 #ifndef MOEBAL_H
 #define MOEBAL_H
@@ -77,7 +77,20 @@ extern "C" {
 enum mb_dtype {
   MB_F32 = 0,       /* IEEE binary32 */
   MB_BF16 = 1,      /* bfloat16 */
-  MB_FP8_E4M3 = 2   /* OCP fp8 e4m3fn, one fp32 scale per 128 elements */
+  MB_FP8_E4M3 = 2,  /* OCP fp8 e4m3fn, one fp32 scale per 128 elements */
+  MB_MX4 = 3        /* packed e2m1, one e8m0 scale byte per 32 (mb_quantize_mx4) */
+};
+
+/* How mb_route turns logits into scores. */
+enum mb_score {
+  MB_SCORE_SOFTMAX = 0, /* over all experts of the token */
+  MB_SCORE_SIGMOID = 1  /* of each logit by itself */
+};
+
+/* What mb_quantize_mx4 applies to a row before it quantises it. */
+enum mb_act {
+  MB_ACT_NONE = 0,
+  MB_ACT_SWIGLU = 1 /* silu(gate) * up of a row [gate | up] of twice the length */
 };
 
 /* Return codes. */
@@ -324,9 +337,12 @@ int mb_plan_ex(const mb_dims* dims, const int32_t* ids_dev, const mb_plan_option
  * Dispatch [MoonEP, "What MoonEP enforces and how": tokens written into
  * fixed-shape expert-grouped buffers]: buf[pos[t][k]] = x[t] for every pair.
  *  x_dev          [N, H] rows of dtype_in.
- *  x_scale_dev    [N, H/128] fp32 scales for MB_FP8_E4M3 rows, else NULL.
+ *  x_scale_dev    [N, H/128] fp32 scales for MB_FP8_E4M3 rows; for MB_MX4
+ *                 rows (H/2 bytes each) their [N, H/32] e8m0 scale bytes, 4-byte
+ *                 aligned; else NULL.
  *  buf_dev        [P*cap, H] rows of dtype_in; padding rows are not written.
- *  buf_scale_dev  [P*cap, H/128] fp32 for MB_FP8_E4M3, else NULL.
+ *  buf_scale_dev  [P*cap, H/128] fp32 for MB_FP8_E4M3, [P*cap, H/32] bytes for
+ *                 MB_MX4, 4-byte aligned; else NULL.
  * Reads plan->pos and plan->status. Row pointers must be 16-byte aligned.
  */
 int mb_dispatch(const mb_dims* dims, const mb_plan_bufs* plan, const void* x_dev,
@@ -364,6 +380,128 @@ int mb_combine(const mb_dims* dims, const mb_plan_bufs* plan, const void* y_exp_
 int mb_combine_fp8(const mb_dims* dims, const mb_plan_bufs* plan, const uint8_t* y_exp_dev,
                    const float* y_scale_dev, const float* w_dev, void* y_dev,
                    hipStream_t stream);
+
+/* What mb_route computes for one batch of tokens. */
+typedef struct mb_route_params {
+  int32_t n_tokens;   /* N in [0, 2^26 - 16] */
+  int32_t n_experts;  /* E in [1, 1024] */
+  int32_t top_k;      /* K in [1, min(32, E)], at most top_groups * E / n_groups */
+  int32_t dtype;      /* logits: MB_F32 or MB_BF16 */
+  int32_t score;      /* mb_score */
+  int32_t n_groups;   /* G in [1, 64], E % G == 0: expert e is in group e / (E/G) */
+  int32_t top_groups; /* groups a token may choose from, in [1, G] */
+  int32_t group_top;  /* a group's score: the sum of its 1 or 2 largest choice values (2: E/G >= 2), -inf with
+                         fewer unmasked experts */
+  int32_t renorm;     /* non-zero: the K weights are divided by their sum */
+  float scale;        /* finite factor of every weight */
+} mb_route_params;
+
+/*
+ * Route: the router's logits to the ids and gate weights mb_plan and
+ * mb_combine take.
+ *   score_e  = softmax or sigmoid of the token's logits;
+ *   choice_e = score_e + bias_e (bias counts for the choice only);
+ * the top_groups groups of highest group score are open (ties: the lowest
+ * group); the K open experts of highest choice value are taken in descending
+ * order (ties: the lowest id); w_k = score, divided by the sum of the K when
+ * renorm is set, times scale. The choice is the one exact arithmetic on the
+ * given logits and biases makes: values too close for binary32 are compared
+ * in binary64. The weights are binary32.
+ * Masks: an expert whose logit or bias is -inf or NaN is masked. Its choice
+ * value is -inf, so it is taken only when fewer than K others are open (ids
+ * ascending, always K distinct ids), and its weight is 0; the softmax sums
+ * over the experts whose logit does not mask them. A row that masks every
+ * expert gets weight 0 throughout. Softmax logits of +inf share the whole
+ * probability.
+ *  logits_dev [N, E] of prm->dtype.
+ *  bias_dev   [E] fp32, or NULL for none.
+ *  ids_dev    [N*K] int32 out.
+ *  w_dev      [N*K] fp32 out.
+ * prm is host memory, read during the call only. logits must be 16-byte
+ * aligned, the others 4-byte.
+ */
+int mb_route(const mb_route_params* prm, const void* logits_dev, const float* bias_dev,
+             int32_t* ids_dev, float* w_dev, hipStream_t stream);
+
+/* Largest row length of mb_rmsnorm_fp8. */
+#define MB_MAX_NORM_HIDDEN 16384
+
+/*
+ * Root-mean-square norm with the residual's addition and an fp8 output: the
+ * rows mb_dispatch takes as MB_FP8_E4M3. For every row, in fp32:
+ *   h = x + residual (h = x without one);
+ *   y = h * weight / sqrt(sum(h^2) / H + eps);
+ *   scale_b = max|y| / 448 over each block b of 128 elements,
+ *   q = e4m3fn(y / scale), round to nearest even, saturating at 448.
+ * A block whose largest magnitude is below 2^-110 gets scale 1 and zeros. A
+ * row holding a NaN or an infinity, or whose sum of squares overflows
+ * binary32, gets NaN codes and scales (and NaN rows in y_dev). A zero row gives zeros
+ * also when eps is 0.
+ *  n_rows, hidden    n_rows in [0, 2^24 - 4]; H % 128 == 0, H <= 16384.
+ *  dtype             MB_F32 or MB_BF16: x, residual, weight, residual_out, y.
+ *  eps               finite, >= 0.
+ *  residual_dev      [n_rows, H], or NULL: no addition.
+ *  residual_out_dev  [n_rows, H] h rounded to dtype (round to nearest even);
+ *                    NULL to not store it. May be x_dev or residual_dev
+ *                    themselves (in place); no other overlap is allowed.
+ *                    Needs residual_dev.
+ *  y_dev             [n_rows, H] the normed rows in dtype, or NULL.
+ *  q_dev             [n_rows, H] fp8 codes.
+ *  q_scale_dev       [n_rows, H/128] fp32 scales.
+ * All pointers 16-byte aligned but q_scale (4).
+ */
+int mb_rmsnorm_fp8(int32_t n_rows, int32_t hidden, int32_t dtype, float eps, const void* x_dev,
+                   const void* residual_dev, const void* weight_dev, void* residual_out_dev,
+                   void* y_dev, uint8_t* q_dev, float* q_scale_dev, hipStream_t stream);
+
+/*
+ * Microscaled 4-bit rows (OCP Microscaling Formats v1.0, MXFP4): elements
+ * e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; element 2i in the
+ * low nibble of byte i), one e8m0 scale byte s = 2^(s - 127) per 32 elements
+ * of a row.
+ * Quantise: s = 127 + floor(log2(max|v|)) - 2 clamped to [0, 254], element =
+ * v / 2^(s - 127) rounded to nearest even, saturating at 6. An all-zero
+ * block has s = 0. A block holding a NaN or an infinity has s = 255 (NaN)
+ * and zero elements.
+ *  act         MB_ACT_NONE: v = x; MB_ACT_SWIGLU: x rows are [gate | up] of
+ *              2*hidden elements and v = gate / (1 + exp(-gate)) * up in fp32.
+ *  x_dev       [n_rows, hidden or 2*hidden] of dtype (MB_F32, MB_BF16).
+ *  row_src_dev [n_rows] int32 or NULL: rows with a negative entry (the
+ *              padding rows of a plan's row_src) are neither read nor written.
+ *  q_dev       [n_rows, hidden/2], q_scale_dev [n_rows, hidden/32].
+ * hidden % 32 == 0, n_rows >= 0 and n_rows * ceil(hidden / 512) <= 2^26 - 16;
+ * x and q 16-byte aligned, row_src 4-byte.
+ */
+int mb_quantize_mx4(int32_t n_rows, int32_t hidden, int32_t dtype, int32_t act, const void* x_dev,
+                    const int32_t* row_src_dev, uint8_t* q_dev, uint8_t* q_scale_dev,
+                    hipStream_t stream);
+
+/* The values of microscaled 4-bit rows, as rows of dtype (MB_F32 or MB_BF16;
+ * both hold them exactly). A scale of 255 gives NaN. Layouts, limits and
+ * alignment as mb_quantize_mx4. */
+int mb_dequantize_mx4(int32_t n_rows, int32_t hidden, int32_t dtype, const uint8_t* q_dev,
+                      const uint8_t* q_scale_dev, void* x_dev, hipStream_t stream);
+
+/*
+ * Experts' products over the dispatch layout: for every row p of every slot,
+ *   y[p][j] = sum_i a[p][i] * w[e][j][i],  e = the expert the slot holds
+ * (slot i < Eh of rank r: r*Eh + i; replica slot i - Eh: rep_expert), from
+ * microscaled 4-bit rows and weights, accumulated in fp32, stored as
+ * dims->dtype_out (bf16: round to nearest even). Rows no slot covers are not
+ * written. An empty slot, or a replica slot holding no expert, costs nothing.
+ *  n_out, k_in  outputs per row and their terms: k_in % 128 == 0, n_out rows
+ *               a multiple of 16 bytes.
+ *  a_dev        [P*cap, k_in/2], a_scale_dev [P*cap, k_in/32].
+ *  w_dev        [E, n_out, k_in/2], w_scale_dev [E, n_out, k_in/32].
+ *  y_dev        [P*cap, n_out] of dtype_out.
+ * Reads plan->cu_seqlens, rep_expert and status; does nothing under a fatal
+ * status. dims gives E, P, R, cap, N*K (the rows expected, which picks the
+ * tile size) and dtype_out; hidden and dtype_in are not used. a, w and y
+ * 16-byte aligned, the scales 4-byte.
+ */
+int mb_expert_mx4(const mb_dims* dims, const mb_plan_bufs* plan, int32_t n_out, int32_t k_in,
+                  const uint8_t* a_dev, const uint8_t* a_scale_dev, const uint8_t* w_dev,
+                  const uint8_t* w_scale_dev, void* y_dev, hipStream_t stream);
 
 /*
  * Copy status[4] to host_status (host memory) after the work enqueued on

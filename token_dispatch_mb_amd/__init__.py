@@ -16,8 +16,8 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoebal.so")
 
-F32, BF16, FP8_E4M3 = 0, 1, 2
-DTYPES = {"f32": F32, "bf16": BF16, "fp8": FP8_E4M3}
+F32, BF16, FP8_E4M3, MX4 = 0, 1, 2, 3
+DTYPES = {"f32": F32, "bf16": BF16, "fp8": FP8_E4M3, "mx4": MX4}
 TORCH_DTYPES = {F32: torch.float32, BF16: torch.bfloat16, FP8_E4M3: torch.uint8}
 ELT_BYTES = {F32: 4, BF16: 2, FP8_E4M3: 1}
 
@@ -130,9 +130,45 @@ _lib.mb_combine_fp8.restype = ctypes.c_int
 _lib.mb_plan_status.argtypes = [ctypes.POINTER(_PlanBufsC), _vp, _i32p]
 _lib.mb_plan_status.restype = ctypes.c_int
 
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
+ACT_NONE, ACT_SWIGLU = 0, 1
+ACTS = {"none": ACT_NONE, "swiglu": ACT_SWIGLU}
+MAX_GROUPS, MAX_NORM_HIDDEN = 64, 16384
+
+
+class RouteParams(ctypes.Structure):
+    """mb_route_params."""
+
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "n_tokens", "n_experts", "top_k", "dtype", "score", "n_groups", "top_groups", "group_top",
+        "renorm")] + [("scale", ctypes.c_float)]
+
+    @classmethod
+    def make(cls, n_tokens, n_experts, top_k, dtype="f32", score="softmax", n_groups=1,
+             top_groups=1, group_top=1, renorm=True, scale=1.0) -> "RouteParams":
+        return cls(n_tokens, n_experts, top_k, DTYPES[dtype] if isinstance(dtype, str) else dtype,
+                   SCORES[score] if isinstance(score, str) else score, n_groups, top_groups,
+                   group_top, int(bool(renorm)), scale)
+
+
+_i32, _f32 = ctypes.c_int32, ctypes.c_float
+_lib.mb_route.argtypes = [ctypes.POINTER(RouteParams), _vp, _vp, _vp, _vp, _vp]
+_lib.mb_route.restype = ctypes.c_int
+_lib.mb_rmsnorm_fp8.argtypes = [_i32, _i32, _i32, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+_lib.mb_rmsnorm_fp8.restype = ctypes.c_int
+_lib.mb_quantize_mx4.argtypes = [_i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp]
+_lib.mb_quantize_mx4.restype = ctypes.c_int
+_lib.mb_dequantize_mx4.argtypes = [_i32, _i32, _i32, _vp, _vp, _vp, _vp]
+_lib.mb_dequantize_mx4.restype = ctypes.c_int
+_lib.mb_expert_mx4.argtypes = [ctypes.POINTER(Dims), ctypes.POINTER(_PlanBufsC), _i32, _i32, _vp,
+                               _vp, _vp, _vp, _vp, _vp]
+_lib.mb_expert_mx4.restype = ctypes.c_int
+
 EXPORTS = ("mb_version", "mb_strerror", "mb_plan_workspace_bytes", "mb_plan",
            "mb_plan_noalloc", "mb_plan_weighted", "mb_drift_state_bytes", "mb_plan_drift", "mb_plan_ex",
-           "mb_dispatch", "mb_combine", "mb_combine_fp8", "mb_plan_status")
+           "mb_dispatch", "mb_combine", "mb_combine_fp8", "mb_plan_status", "mb_route",
+           "mb_rmsnorm_fp8", "mb_quantize_mx4", "mb_dequantize_mx4", "mb_expert_mx4")
 ST_REPLANNED = 16
 ST_GUARDED = 32
 NOALLOC_WS_BYTES = 4 << 20
@@ -322,13 +358,17 @@ def plan_noalloc(dims: Dims, ids: torch.Tensor, bufs: PlanBuffers, stream=None) 
 def dispatch(dims: Dims, bufs: PlanBuffers, x: torch.Tensor, buf: torch.Tensor,
              x_scale: torch.Tensor | None = None, buf_scale: torch.Tensor | None = None,
              stream=None) -> None:
-    """mb_dispatch: buf[pos[t][k]] = x[t] (and the fp8 scale rows)."""
-    row = dims.hidden * ELT_BYTES.get(dims.dtype_in, 0)
+    """mb_dispatch: buf[pos[t][k]] = x[t] (and the scale rows: fp32
+    [N, H/128] for fp8, uint8 [N, H/32] for 4-bit rows)."""
+    row = dims.hidden // 2 if dims.dtype_in == MX4 else dims.hidden * ELT_BYTES.get(dims.dtype_in, 0)
     _check(x, "x", nbytes=dims.n_tokens * row)
     _check(buf, "buf", nbytes=dims.rows * row)
     if dims.dtype_in == FP8_E4M3:
         _check(x_scale, "x_scale", torch.float32, numel=dims.n_tokens * (dims.hidden // 128))
         _check(buf_scale, "buf_scale", torch.float32, numel=dims.rows * (dims.hidden // 128))
+    elif dims.dtype_in == MX4:
+        _check(x_scale, "x_scale", torch.uint8, numel=dims.n_tokens * (dims.hidden // 32))
+        _check(buf_scale, "buf_scale", torch.uint8, numel=dims.rows * (dims.hidden // 32))
     rc = _lib.mb_dispatch(ctypes.byref(dims), ctypes.byref(bufs.c_struct(dims)), _ptr(x),
                           _ptr(x_scale), _ptr(buf), _ptr(buf_scale),
                           _stream(stream, x, buf, x_scale, buf_scale, bufs.status))
@@ -383,6 +423,123 @@ def combine_fp8(dims: Dims, bufs: PlanBuffers, y_exp: torch.Tensor, y_scale: tor
                              _stream(stream, y_exp, y_scale, w, y, bufs.status))
     if rc != OK:
         raise MoebalError("mb_combine_fp8", rc)
+
+
+def route(prm: RouteParams, logits: torch.Tensor, ids: torch.Tensor, w: torch.Tensor,
+          bias: torch.Tensor | None = None, stream=None) -> None:
+    """mb_route: router logits [N, E] to expert ids (int32) and gate weights
+    (fp32) [N, K], the inputs of ``plan`` and ``combine``."""
+    n = prm.n_tokens
+    _check(logits, "logits", _row_dtype(prm.dtype), numel=n * prm.n_experts)
+    _check(ids, "ids", torch.int32, numel=n * prm.top_k)
+    _check(w, "w", torch.float32, numel=n * prm.top_k)
+    if bias is not None:
+        _check(bias, "bias", torch.float32, numel=prm.n_experts)
+    rc = _lib.mb_route(ctypes.byref(prm), _ptr(logits), _ptr(bias), _ptr(ids), _ptr(w),
+                       _stream(stream, logits, bias, ids, w))
+    if rc != OK:
+        raise MoebalError("mb_route", rc)
+
+
+def _row_dtype(code: int) -> torch.dtype:
+    if code not in (F32, BF16):
+        raise ValueError(f"rows must be f32 or bf16 (dtype code {code})")
+    return TORCH_DTYPES[code]
+
+
+def _rows(t, name: str) -> tuple[int, int, int]:
+    """(rows, row length, dtype code) of a 2-D f32 or bf16 GPU tensor."""
+    _check(t, name)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions (it has {t.dim()})")
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name} must be torch.float32 or torch.bfloat16 (it is {t.dtype})")
+    return t.shape[0], t.shape[1], F32 if t.dtype == torch.float32 else BF16
+
+
+def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    lo, hi = a.data_ptr(), b.data_ptr()
+    return lo < hi + _nbytes(b) and hi < lo + _nbytes(a)
+
+
+def rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float, q: torch.Tensor,
+                q_scale: torch.Tensor, residual: torch.Tensor | None = None,
+                residual_out: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                stream=None) -> None:
+    """mb_rmsnorm_fp8: root-mean-square norm of x [N, H] (plus ``residual``)
+    to fp8 rows q (uint8 [N, H]) with fp32 scales [N, H/128], the rows
+    ``dispatch`` takes; optionally the sum x + residual (``residual_out``,
+    which may be x or residual themselves) and the normed rows ``y``."""
+    n, h, code = _rows(x, "x")
+    _check(weight, "weight", x.dtype, numel=h)
+    _check(q, "q", torch.uint8, numel=n * h)
+    _check(q_scale, "q_scale", torch.float32, numel=n * (h // 128))
+    for name, t in (("residual", residual), ("residual_out", residual_out), ("y", y)):
+        if t is not None:
+            _check(t, name, x.dtype, numel=n * h)
+    ins = [t for t in (x, residual, weight) if t is not None]
+    outs = [t for t in (residual_out, y, q, q_scale) if t is not None]
+    for i, o in enumerate(outs):
+        for t in ins + outs[:i]:
+            in_place = o is residual_out and t is not weight and o.data_ptr() == t.data_ptr()
+            if n * h and _overlap(o, t) and not in_place:
+                raise ValueError("outputs must not overlap each other or the inputs (residual_out "
+                                 "may be x or residual themselves)")
+    rc = _lib.mb_rmsnorm_fp8(n, h, code, eps, _ptr(x), _ptr(residual), _ptr(weight),
+                             _ptr(residual_out), _ptr(y), _ptr(q), _ptr(q_scale),
+                             _stream(stream, x, residual, weight, residual_out, y, q, q_scale))
+    if rc != OK:
+        raise MoebalError("mb_rmsnorm_fp8", rc)
+
+
+def quantize_mx4(x: torch.Tensor, q: torch.Tensor, q_scale: torch.Tensor, act: str = "none",
+                 row_src: torch.Tensor | None = None, stream=None) -> None:
+    """mb_quantize_mx4: rows x [M, H] to packed e2m1 codes (uint8 [M, H/2])
+    and e8m0 scale bytes [M, H/32]; with act="swiglu" x rows are [gate | up]
+    of 2H. Rows with a negative ``row_src`` entry are skipped."""
+    m, h, code = _rows(x, "x")
+    a = ACTS[act]
+    if a == ACT_SWIGLU:
+        if h % 2:
+            raise ValueError(f"swiglu rows must have an even length (it is {h})")
+        h //= 2
+    _check(q, "q", torch.uint8, numel=m * (h // 2))
+    _check(q_scale, "q_scale", torch.uint8, numel=m * (h // 32))
+    if row_src is not None:
+        _check(row_src, "row_src", torch.int32, numel=m)
+    rc = _lib.mb_quantize_mx4(m, h, code, a, _ptr(x), _ptr(row_src), _ptr(q), _ptr(q_scale),
+                              _stream(stream, x, row_src, q, q_scale))
+    if rc != OK:
+        raise MoebalError("mb_quantize_mx4", rc)
+
+
+def dequantize_mx4(q: torch.Tensor, q_scale: torch.Tensor, x: torch.Tensor, stream=None) -> None:
+    """mb_dequantize_mx4: packed 4-bit rows back to rows x [M, H]."""
+    m, h, code = _rows(x, "x")
+    _check(q, "q", torch.uint8, numel=m * (h // 2))
+    _check(q_scale, "q_scale", torch.uint8, numel=m * (h // 32))
+    rc = _lib.mb_dequantize_mx4(m, h, code, _ptr(q), _ptr(q_scale), _ptr(x),
+                                _stream(stream, q, q_scale, x))
+    if rc != OK:
+        raise MoebalError("mb_dequantize_mx4", rc)
+
+
+def expert_mx4(dims: Dims, bufs: PlanBuffers, n_out: int, k_in: int, a: torch.Tensor,
+               a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, y: torch.Tensor,
+               stream=None) -> None:
+    """mb_expert_mx4: y[p] = a[p] @ w[expert of p's slot].T over the plan's
+    rows, from packed 4-bit rows a [P*cap, k_in/2] and weights
+    [E, n_out, k_in/2] with their scale bytes (one per 32)."""
+    _check(a, "a", torch.uint8, numel=dims.rows * (k_in // 2))
+    _check(a_scale, "a_scale", torch.uint8, numel=dims.rows * (k_in // 32))
+    _check(w, "w", torch.uint8, numel=dims.n_experts * n_out * (k_in // 2))
+    _check(w_scale, "w_scale", torch.uint8, numel=dims.n_experts * n_out * (k_in // 32))
+    _check(y, "y", TORCH_DTYPES.get(dims.dtype_out), numel=dims.rows * n_out)
+    rc = _lib.mb_expert_mx4(ctypes.byref(dims), ctypes.byref(bufs.c_struct(dims)), n_out, k_in,
+                            _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), _ptr(y),
+                            _stream(stream, a, a_scale, w, w_scale, y, bufs.status))
+    if rc != OK:
+        raise MoebalError("mb_expert_mx4", rc)
 
 
 def plan_status(bufs: PlanBuffers, stream=None):

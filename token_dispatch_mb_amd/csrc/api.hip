@@ -65,21 +65,21 @@ static int validate(const mb_dims* d) {
   if (d->hidden < 1 || d->cap < 1) return MB_ERR_INVALID_ARG;
   if ((int64_t)d->n_tokens * d->top_k > INT32_MAX) return MB_ERR_INVALID_ARG;
   if ((int64_t)d->n_ranks * d->cap > INT32_MAX) return MB_ERR_INVALID_ARG;
-  const int64_t bin = elt_bytes(d->dtype_in);
-  if (!bin) return MB_ERR_INVALID_ARG;
+  const int64_t row_in = row_bytes(d->dtype_in, d->hidden);
+  if (!row_in) return MB_ERR_INVALID_ARG;
   if (d->dtype_out != MB_F32 && d->dtype_out != MB_BF16) return MB_ERR_INVALID_ARG;
-  if ((int64_t)d->hidden * bin % 16 || (int64_t)d->hidden * elt_bytes(d->dtype_out) % 16)
+  if (row_in % 16 || (int64_t)d->hidden * elt_bytes(d->dtype_out) % 16)
     return MB_ERR_INVALID_ARG;
-  if ((int64_t)d->hidden * bin / 16 > INT32_MAX) return MB_ERR_INVALID_ARG;
+  if (row_in / 16 > INT32_MAX) return MB_ERR_INVALID_ARG;
   // dispatch runs one wave per 1 KiB part of every token row, the combines
   // one per 512 bytes of output row (at least as many as per 512 fp8
   // elements of an expert row, which the fp8 combine uses)
-  if ((int64_t)d->n_tokens * (((int64_t)d->hidden * bin / 16 + 63) / 64) > INT32_MAX)
+  if ((int64_t)d->n_tokens * ((row_in / 16 + 63) / 64) > INT32_MAX)
     return MB_ERR_INVALID_ARG;
   if ((int64_t)d->n_tokens * (((int64_t)d->hidden * elt_bytes(d->dtype_out) / 8 + 63) / 64) >
       INT32_MAX)
     return MB_ERR_INVALID_ARG;
-  if (d->dtype_in == MB_FP8_E4M3 && d->hidden % 128) return MB_ERR_INVALID_ARG;
+  if (scaled_rows(d->dtype_in) && d->hidden % 128) return MB_ERR_INVALID_ARG;
   return MB_OK;
 }
 
@@ -90,6 +90,7 @@ static bool plan_ptrs_ok(const mb_dims* d, const mb_plan_bufs* o) {
 }
 
 static bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+static bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
 extern "C" {
 
@@ -275,7 +276,9 @@ int mb_dispatch(const mb_dims* dims, const mb_plan_bufs* plan, const void* x_dev
   if (!plan || (dims->n_tokens > 0 && (!plan->pos || !x_dev)) || !plan->status || !buf_dev)
     return MB_ERR_INVALID_ARG;
   if (!aligned16(x_dev) || !aligned16(buf_dev)) return MB_ERR_INVALID_ARG;
-  if (dims->dtype_in == MB_FP8_E4M3 && (!x_scale_dev || !buf_scale_dev)) return MB_ERR_INVALID_ARG;
+  if (scaled_rows(dims->dtype_in) && (!x_scale_dev || !buf_scale_dev)) return MB_ERR_INVALID_ARG;
+  if (dims->dtype_in == MB_MX4 && (!aligned4(x_scale_dev) || !aligned4(buf_scale_dev)))
+    return MB_ERR_INVALID_ARG;
   return launch_dispatch(*dims, *plan, x_dev, x_scale_dev, buf_dev, buf_scale_dev, stream) ==
                  hipSuccess
              ? MB_OK
@@ -307,6 +310,106 @@ int mb_combine_fp8(const mb_dims* dims, const mb_plan_bufs* plan, const uint8_t*
     return MB_ERR_INVALID_ARG;
   return launch_combine_fp8(*dims, *plan, y_exp_dev, y_scale_dev, w_dev, y_dev, stream) ==
                  hipSuccess
+             ? MB_OK
+             : MB_ERR_HIP;
+}
+
+int mb_route(const mb_route_params* prm, const void* logits_dev, const float* bias_dev,
+             int32_t* ids_dev, float* w_dev, hipStream_t stream) {
+  if (!prm) return MB_ERR_INVALID_ARG;
+  const mb_route_params& p = *prm;
+  if (p.n_tokens < 0 || p.n_experts < 1 || p.n_experts > kMaxExperts) return MB_ERR_INVALID_ARG;
+  if (p.n_groups < 1 || p.n_groups > kMaxGroups || p.n_experts % p.n_groups)
+    return MB_ERR_INVALID_ARG;
+  const int size = p.n_experts / p.n_groups;
+  if (p.top_groups < 1 || p.top_groups > p.n_groups) return MB_ERR_INVALID_ARG;
+  if (p.group_top < 1 || p.group_top > 2 || p.group_top > size) return MB_ERR_INVALID_ARG;
+  if (p.top_k < 1 || p.top_k > kMaxTopK || p.top_k > p.top_groups * size)
+    return MB_ERR_INVALID_ARG;
+  if (p.dtype != MB_F32 && p.dtype != MB_BF16) return MB_ERR_INVALID_ARG;
+  if (p.score != MB_SCORE_SOFTMAX && p.score != MB_SCORE_SIGMOID) return MB_ERR_INVALID_ARG;
+  if (!(p.scale - p.scale == 0.0f)) return MB_ERR_INVALID_ARG;  // NaN or infinite
+  if (p.n_tokens > kMaxWaves) return MB_ERR_INVALID_ARG;
+  if (p.n_tokens > 0 && (!logits_dev || !ids_dev || !w_dev)) return MB_ERR_INVALID_ARG;
+  if (!aligned16(logits_dev) || !aligned4(bias_dev) || !aligned4(ids_dev) || !aligned4(w_dev))
+    return MB_ERR_INVALID_ARG;
+  return launch_route(p, logits_dev, bias_dev, ids_dev, w_dev, stream) == hipSuccess ? MB_OK
+                                                                                     : MB_ERR_HIP;
+}
+
+int mb_rmsnorm_fp8(int32_t n_rows, int32_t hidden, int32_t dtype, float eps, const void* x_dev,
+                   const void* residual_dev, const void* weight_dev, void* residual_out_dev,
+                   void* y_dev, uint8_t* q_dev, float* q_scale_dev, hipStream_t stream) {
+  if (n_rows < 0 || n_rows > kMaxWaves / 4 || hidden < 128 || hidden % 128 ||
+      hidden > MB_MAX_NORM_HIDDEN)
+    return MB_ERR_INVALID_ARG;
+  if (dtype != MB_F32 && dtype != MB_BF16) return MB_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f) || !(eps - eps == 0.0f)) return MB_ERR_INVALID_ARG;
+  if (residual_out_dev && !residual_dev) return MB_ERR_INVALID_ARG;
+  if (n_rows > 0 && (!x_dev || !weight_dev || !q_dev || !q_scale_dev)) return MB_ERR_INVALID_ARG;
+  if (!aligned16(x_dev) || !aligned16(residual_dev) || !aligned16(weight_dev) ||
+      !aligned16(residual_out_dev) || !aligned16(y_dev) || !aligned16(q_dev) ||
+      !aligned4(q_scale_dev))
+    return MB_ERR_INVALID_ARG;
+  return launch_rmsnorm_fp8(n_rows, hidden, dtype == MB_BF16, eps, x_dev, residual_dev, weight_dev,
+                            residual_out_dev, y_dev, q_dev, q_scale_dev, stream) == hipSuccess
+             ? MB_OK
+             : MB_ERR_HIP;
+}
+
+// Sizes shared by the two directions of the 4-bit rows.
+static bool mx4_rows_ok(int32_t n_rows, int32_t hidden, int32_t dtype) {
+  if (n_rows < 0 || hidden < 32 || hidden % 32) return false;
+  if (dtype != MB_F32 && dtype != MB_BF16) return false;
+  // a wave per 512 elements of a row, in launches of fewer than 2^32 threads
+  return (int64_t)n_rows * ((hidden + 511) / 512) <= kMaxWaves;
+}
+
+int mb_quantize_mx4(int32_t n_rows, int32_t hidden, int32_t dtype, int32_t act, const void* x_dev,
+                    const int32_t* row_src_dev, uint8_t* q_dev, uint8_t* q_scale_dev,
+                    hipStream_t stream) {
+  if (!mx4_rows_ok(n_rows, hidden, dtype)) return MB_ERR_INVALID_ARG;
+  if (act != MB_ACT_NONE && act != MB_ACT_SWIGLU) return MB_ERR_INVALID_ARG;
+  if (n_rows > 0 && (!x_dev || !q_dev || !q_scale_dev)) return MB_ERR_INVALID_ARG;
+  if (!aligned16(x_dev) || !aligned16(q_dev) || !aligned4(row_src_dev)) return MB_ERR_INVALID_ARG;
+  return launch_quantize_mx4(n_rows, hidden, dtype == MB_BF16, act == MB_ACT_SWIGLU, x_dev,
+                             row_src_dev, q_dev, q_scale_dev, stream) == hipSuccess
+             ? MB_OK
+             : MB_ERR_HIP;
+}
+
+int mb_dequantize_mx4(int32_t n_rows, int32_t hidden, int32_t dtype, const uint8_t* q_dev,
+                      const uint8_t* q_scale_dev, void* x_dev, hipStream_t stream) {
+  if (!mx4_rows_ok(n_rows, hidden, dtype)) return MB_ERR_INVALID_ARG;
+  if (n_rows > 0 && (!x_dev || !q_dev || !q_scale_dev)) return MB_ERR_INVALID_ARG;
+  if (!aligned16(x_dev) || !aligned16(q_dev)) return MB_ERR_INVALID_ARG;
+  return launch_dequantize_mx4(n_rows, hidden, dtype == MB_BF16, q_dev, q_scale_dev, x_dev,
+                               stream) == hipSuccess
+             ? MB_OK
+             : MB_ERR_HIP;
+}
+
+int mb_expert_mx4(const mb_dims* dims, const mb_plan_bufs* plan, int32_t n_out, int32_t k_in,
+                  const uint8_t* a_dev, const uint8_t* a_scale_dev, const uint8_t* w_dev,
+                  const uint8_t* w_scale_dev, void* y_dev, hipStream_t stream) {
+  const int rc = validate(dims);
+  if (rc != MB_OK) return rc;
+  if (n_out < 1 || n_out > kMaxExpertDim || n_out * elt_bytes(dims->dtype_out) % 16)
+    return MB_ERR_INVALID_ARG;
+  if (k_in < 128 || k_in > kMaxExpertDim || k_in % 128) return MB_ERR_INVALID_ARG;
+  if (!plan || !plan->status || !plan->cu_seqlens ||
+      (dims->slots_per_rank > 0 && !plan->rep_expert) || !a_dev || !a_scale_dev || !w_dev ||
+      !w_scale_dev || !y_dev)
+    return MB_ERR_INVALID_ARG;
+  if (!aligned16(a_dev) || !aligned16(w_dev) || !aligned16(y_dev) || !aligned4(a_scale_dev) ||
+      !aligned4(w_scale_dev))
+    return MB_ERR_INVALID_ARG;
+  const Geometry g = geometry(*dims);
+  // output tiles of at least 16 rows x 16 columns are numbered in int32
+  const int64_t row_tiles = (int64_t)dims->n_ranks * dims->cap / 16 + (int64_t)dims->n_ranks * g.NS;
+  if (row_tiles * ((n_out + 15) / 16) > INT32_MAX) return MB_ERR_INVALID_ARG;
+  return launch_expert_mx4(*dims, g, *plan, n_out, k_in, a_dev, a_scale_dev, w_dev, w_scale_dev,
+                           y_dev, stream) == hipSuccess
              ? MB_OK
              : MB_ERR_HIP;
 }

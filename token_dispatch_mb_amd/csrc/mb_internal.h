@@ -18,6 +18,9 @@ constexpr int kMaxRanks = 64;     // one wave lane per logical rank in k_plan
 constexpr int kMaxExperts = 1024; // LDS: kWaves * E * 8 bytes of token masks
 constexpr int kMaxTopK = 32;
 constexpr int kMaxSlots = 16;
+constexpr int kMaxGroups = 64;             // one wave lane per group in k_route
+constexpr int kMaxWaves = (1 << 26) - 16;  // waves of one launch: fewer than 2^32 threads
+constexpr int kMaxExpertDim = 1 << 20;     // n_out and k_in of the experts' products
 // Block-count tables k_plan and k_assign sum directly instead of running
 // k_scan: at most this many routing blocks per source and block counts.
 constexpr int kSmallTableBlocks = 4;
@@ -119,6 +122,21 @@ hipError_t launch_combine(const mb_dims& d, const mb_plan_bufs& o, const void* y
 hipError_t launch_combine_fp8(const mb_dims& d, const mb_plan_bufs& o, const void* y_exp,
                               const float* y_scale, const float* w, void* y, hipStream_t st);
 
+hipError_t launch_route(const mb_route_params& p, const void* logits, const float* bias,
+                        int32_t* ids, float* w, hipStream_t st);
+hipError_t launch_rmsnorm_fp8(int32_t n_rows, int32_t hidden, bool bf16, float eps, const void* x,
+                              const void* res, const void* weight, void* res_out, void* y,
+                              uint8_t* q, float* q_scale, hipStream_t st);
+hipError_t launch_quantize_mx4(int32_t n_rows, int32_t hidden, bool bf16, bool swiglu,
+                               const void* x, const int32_t* row_src, uint8_t* q,
+                               uint8_t* q_scale, hipStream_t st);
+hipError_t launch_dequantize_mx4(int32_t n_rows, int32_t hidden, bool bf16, const uint8_t* q,
+                                 const uint8_t* q_scale, void* x, hipStream_t st);
+hipError_t launch_expert_mx4(const mb_dims& d, const Geometry& g, const mb_plan_bufs& o,
+                             int32_t n_out, int32_t k_in, const uint8_t* a,
+                             const uint8_t* a_scale, const uint8_t* w, const uint8_t* w_scale,
+                             void* y, hipStream_t st);
+
 // Launch KERNEL<K> for the top-K values with a specialised kernel, KERNEL<0>
 // (runtime K) otherwise.
 #define MB_DISPATCH_TOPK(K, KERNEL, GRID, BLOCK, SHMEM, STREAM, ...)                     \
@@ -135,5 +153,15 @@ hipError_t launch_combine_fp8(const mb_dims& d, const mb_plan_bufs& o, const voi
 inline int64_t elt_bytes(int32_t dtype) {
   return dtype == MB_F32 ? 4 : dtype == MB_BF16 ? 2 : dtype == MB_FP8_E4M3 ? 1 : 0;
 }
+
+// Bytes of a row of `hidden` elements (0: not a row type); 4-bit rows hold
+// two elements in a byte.
+inline int64_t row_bytes(int32_t dtype, int32_t hidden) {
+  return dtype == MB_MX4 ? hidden / 2 : hidden * elt_bytes(dtype);
+}
+
+// Rows with scales: H/128 words of 4 bytes each, one fp32 scale per 128
+// elements (fp8) or four e8m0 bytes (4-bit rows).
+inline bool scaled_rows(int32_t dtype) { return dtype == MB_FP8_E4M3 || dtype == MB_MX4; }
 
 }  // namespace mb

@@ -1,0 +1,109 @@
+// norm.hip — root-mean-square norm with the residual's addition, rows out in
+// fp8 with a scale per 128 elements (mb_rmsnorm_fp8).
+#include <math.h>
+
+#include "mb_internal.h"
+#include "rowio.h"
+#include "wave.h"
+
+namespace mb {
+namespace {
+
+constexpr int kNormThreads = 256;
+constexpr float kE4m3Max = 448.0f;
+
+// One workgroup per row, a lane per 8 consecutive elements, the row in
+// registers between its two passes (sum of squares; scales and codes).
+template <bool kBF16, int CPT>
+__global__ __launch_bounds__(kNormThreads) void k_rmsnorm_fp8(
+    const void* x, const void* res, const void* weight, void* res_out, void* y, uint32_t* q,
+    float* q_scale, int chunks, float eps) {
+  __shared__ float part[kNormThreads / 64];
+  const size_t row = (size_t)blockIdx.x * chunks;
+  float h[CPT][8];
+  float ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    const int c = i * kNormThreads + threadIdx.x;
+    if (c < chunks) {
+      load8<kBF16>(x, row + c, h[i]);
+      if (res) {
+        float r[8];
+        load8<kBF16>(res, row + c, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[i][j] += r[j];
+        if (res_out) store8<kBF16>(res_out, row + c, h[i]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(h[i][j], h[i][j], ss);
+    }
+  }
+  ss = wave_sum_f32(ss);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = ss;
+  __syncthreads();
+  ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kNormThreads / 64; ++i) ss += part[i];
+  const float ms = ss / (float)(chunks * 8) + eps;
+  float inv = ms > 0.0f ? 1.0f / sqrtf(ms) : 0.0f;
+  const bool bad = !(ss < INFINITY);  // a NaN or an infinity in the row, or a sum past binary32
+  if (bad) inv = NAN;
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    const int c = i * kNormThreads + threadIdx.x;
+    if (c < chunks) {
+      float g[8], v[8], amax = 0.0f;
+      load8<kBF16>(weight, c, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] = bad ? NAN : h[i][j] * inv * g[j];
+        amax = fmaxf(amax, fabsf(v[j]));
+      }
+      if (y) store8<kBF16>(y, row + c, v);
+      // 16 lanes of 8 elements share a block
+      amax = row_max_f32(amax);
+      const bool tiny = amax < 0x1p-110f;
+      const float scale = tiny ? 1.0f : amax * (1.0f / kE4m3Max);
+      const float f = tiny ? 0.0f : kE4m3Max / amax;
+      const uint2 o = {fp8x4(v[0], v[1], v[2], v[3], f), fp8x4(v[4], v[5], v[6], v[7], f)};
+      reinterpret_cast<uint2*>(q)[row + c] = bad ? uint2{0x7f7f7f7fu, 0x7f7f7f7fu} : o;
+      if ((threadIdx.x & 15) == 0) q_scale[(row + c) >> 4] = bad ? NAN : scale;
+    }
+  }
+}
+
+template <bool kBF16>
+void launch_norm_t(int n_rows, int hidden, float eps, const void* x, const void* res,
+                   const void* weight, void* res_out, void* y, uint8_t* q, float* q_scale,
+                   hipStream_t st) {
+  const int chunks = hidden / 8;
+  const int cpt = (chunks + kNormThreads - 1) / kNormThreads;
+  uint32_t* q4 = reinterpret_cast<uint32_t*>(q);
+#define MB_N(C)                                                                                  \
+  hipLaunchKernelGGL((k_rmsnorm_fp8<kBF16, C>), dim3(n_rows), dim3(kNormThreads), 0, st, x, res, \
+                     weight, res_out, y, q4, q_scale, chunks, eps)
+  if (cpt <= 1)
+    MB_N(1);
+  else if (cpt <= 2)
+    MB_N(2);
+  else if (cpt <= 4)
+    MB_N(4);
+  else
+    MB_N(8);
+#undef MB_N
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm_fp8(int32_t n_rows, int32_t hidden, bool bf16, float eps, const void* x,
+                              const void* res, const void* weight, void* res_out, void* y,
+                              uint8_t* q, float* q_scale, hipStream_t st) {
+  if (n_rows == 0) return hipSuccess;
+  if (bf16)
+    launch_norm_t<true>(n_rows, hidden, eps, x, res, weight, res_out, y, q, q_scale, st);
+  else
+    launch_norm_t<false>(n_rows, hidden, eps, x, res, weight, res_out, y, q, q_scale, st);
+  return hipGetLastError();
+}
+
+}  // namespace mb

@@ -1,0 +1,55 @@
+// rowio.h — 8-element lane chunks of fp32 / bf16 rows and conversions shared
+// by the norm and the 4-bit row kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace mb {
+
+// fp32 to bf16, round to nearest even, NaN kept quiet.
+__device__ __forceinline__ uint32_t bf16_rne(float f) {
+  const uint32_t b = __float_as_uint(f);
+  if ((b & 0x7fffffffu) > 0x7f800000u) return (b >> 16) | 0x40u;
+  return (b + 0x7fffu + ((b >> 16) & 1u)) >> 16;
+}
+
+// v[0..8) = elements [8c, 8c + 8) of p.
+template <bool kBF16>
+__device__ __forceinline__ void load8(const void* p, size_t c, float* v) {
+  if constexpr (kBF16) {
+    const uint4 u = static_cast<const uint4*>(p)[c];
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+    const float4 a = static_cast<const float4*>(p)[2 * c], b = static_cast<const float4*>(p)[2 * c + 1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+}
+
+template <bool kBF16>
+__device__ __forceinline__ void store8(void* p, size_t c, const float* v) {
+  if constexpr (kBF16) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = bf16_rne(v[2 * i]) | (bf16_rne(v[2 * i + 1]) << 16);
+    static_cast<uint4*>(p)[c] = uint4{w[0], w[1], w[2], w[3]};
+  } else {
+    static_cast<float4*>(p)[2 * c] = float4{v[0], v[1], v[2], v[3]};
+    static_cast<float4*>(p)[2 * c + 1] = float4{v[4], v[5], v[6], v[7]};
+  }
+}
+
+// Four values times f as e4m3fn bytes, round to nearest even. |v * f| may
+// pass 448 by the rounding of f, never by half a step (16): no overflow.
+__device__ __forceinline__ uint32_t fp8x4(float a, float b, float c, float d, float f) {
+  int o = __builtin_amdgcn_cvt_pk_fp8_f32(a * f, b * f, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c * f, d * f, o, true);
+}
+
+}  // namespace mb

@@ -359,8 +359,8 @@ __global__ __launch_bounds__(kCombThreads) void k_combine_fp8(
 hipError_t launch_dispatch(const mb_dims& d, const mb_plan_bufs& o, const void* x,
                            const float* x_scale, void* buf, float* buf_scale, hipStream_t st) {
   if (d.n_tokens == 0) return hipSuccess;
-  const int rb16 = (int)(d.hidden * elt_bytes(d.dtype_in) / 16);
-  const int nsc = d.dtype_in == MB_FP8_E4M3 ? d.hidden / 128 : 0;
+  const int rb16 = (int)(row_bytes(d.dtype_in, d.hidden) / 16);
+  const int nsc = scaled_rows(d.dtype_in) ? d.hidden / 128 : 0;
   const int rows = d.n_ranks * d.cap;
   const int wpt = (rb16 + 63) / 64;  // waves per token
   const int64_t waves = (int64_t)d.n_tokens * wpt;

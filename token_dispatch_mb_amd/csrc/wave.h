@@ -102,6 +102,41 @@ __device__ __forceinline__ int wave_inclusive_sum(int v) {
   return v;
 }
 
+// Butterfly steps inside a 16-lane row: every lane ends with the row's
+// result (quad_perm [1,0,3,2] and [2,3,0,1], row_half_mirror, row_mirror).
+template <int kCtrl>
+__device__ __forceinline__ float dpp_f32(float v) {
+  return __int_as_float(
+      __builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, 0xf, 0xf, true));
+}
+
+__device__ __forceinline__ float quad_max_f32(float v) {
+  v = fmaxf(v, dpp_f32<0xB1>(v));
+  return fmaxf(v, dpp_f32<0x4E>(v));
+}
+
+__device__ __forceinline__ float row_max_f32(float v) {
+  v = quad_max_f32(v);
+  v = fmaxf(v, dpp_f32<0x141>(v));
+  return fmaxf(v, dpp_f32<0x140>(v));
+}
+
+__device__ __forceinline__ float row_sum_f32(float v) {
+  v += dpp_f32<0xB1>(v);
+  v += dpp_f32<0x4E>(v);
+  v += dpp_f32<0x141>(v);
+  return v + dpp_f32<0x140>(v);
+}
+
+// Sum over the 64 lanes, uniform (every lane active).
+__device__ __forceinline__ float wave_sum_f32(float v) {
+  const int r = __float_as_int(row_sum_f32(v));
+  return (__int_as_float(__builtin_amdgcn_readlane(r, 0)) +
+          __int_as_float(__builtin_amdgcn_readlane(r, 16))) +
+         (__int_as_float(__builtin_amdgcn_readlane(r, 32)) +
+          __int_as_float(__builtin_amdgcn_readlane(r, 48)));
+}
+
 __device__ __forceinline__ int lowest_lane(uint64_t mask) {
   return mask ? __builtin_ctzll(mask) : -1;
 }
