@@ -467,11 +467,32 @@ def test_expert_any_expected_rows(tokens):
 
 @pytest.mark.parametrize("rows", [1, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 129, 255, 256, 257])
 def test_expert_slot_sizes(rows):
-    """Slots of one size, so that a tile ends at, before and behind its rows."""
+    """Slots of one size, so that a tile ends at, before and behind its rows,
+    with every tile size that an expected number of rows picks."""
     P, Eh, cap = 2, 2, 2 * rows + 3
     cu = np.array([[0, rows, 2 * rows], [0, 0, rows]], np.int32)
-    p = Product(rows, P, Eh, 0, cap, 160, 384, plan=(cu, np.full((P, 1), -1, np.int32)))
-    p.check(p.run())
+    for tokens in (2, 60, 200, 1 << 20):
+        for k in (384, 512, 640, 1152):
+            p = Product(rows, P, Eh, 0, cap, 160, k, tokens=tokens,
+                        plan=(cu, np.full((P, 1), -1, np.int32)))
+            p.check(p.run())
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [8, 248, 256, 264, 520, 2056])
+def test_expert_output_sizes(n, out):
+    """Outputs that end inside a tile, in every kernel."""
+    for tokens in (2, 60, 200, 1 << 20):
+        p = Product(n, 2, 3, 1, 300, n, 512, out, tokens=tokens)
+        p.check(p.run())
+
+
+def test_expert_many_tiles_on_each_workgroup():
+    """More tiles than workgroups, odd and even numbers of steps: rows and
+    weights of the next tile are read under the last steps of one."""
+    for k in (512, 640, 768, 896):
+        p = Product(k, 8, 6, 1, 1500, 1288, k, tokens=1 << 20)
+        p.check(p.run())
 
 
 def test_expert_identity_layout():

@@ -7,6 +7,8 @@
 // the rows in memory) and their scale byte. The weights are the first
 // operand, so that a lane ends with four consecutive outputs of one row:
 // column r of the product is row r of the tile, rows 4g..4g+3 its outputs.
+#include <type_traits>
+
 #include "mb_internal.h"
 #include "rowio.h"
 #include "wave.h"
@@ -39,14 +41,17 @@ __device__ __forceinline__ f32x4 mfma_mx4(i32x4 a, i32x4 b, f32x4 c, int sa, int
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, 0, sa, 0, sb);
 }
 
+typedef const __attribute__((address_space(4))) int32_t* plan_ptr;
+
 // Rows [lo, hi) of slot j (r = j / NS), absolute in the buffer, and its
 // expert; empty when it holds none. Only a broken plan needs the clamps.
 __device__ __forceinline__ void slot_rows(const ExpertArgs& p, int j, int& lo, int& hi, int& e) {
   const int r = j / p.NS, i = j - r * p.NS;
-  const int32_t* cu = p.cu + (size_t)r * (p.NS + 1) + i;
+  // the plan does not change under the kernel: constant memory
+  auto cu = (plan_ptr)(p.cu + (size_t)r * (p.NS + 1) + i);
   lo = min(max(cu[0], 0), p.cap);
   hi = min(max(cu[1], lo), p.cap);
-  e = i < p.Eh ? r * p.Eh + i : p.rep[(size_t)r * p.R + i - p.Eh];
+  e = i < p.Eh ? r * p.Eh + i : ((plan_ptr)p.rep)[(size_t)r * p.R + i - p.Eh];
   if ((unsigned)e >= (unsigned)p.E) hi = lo;
   lo += r * p.cap;
   hi += r * p.cap;
@@ -86,17 +91,272 @@ __device__ __forceinline__ int slot_of(const int* first, int nslots, int t) {
     if (first[mid] <= t) lo = mid;
     else hi = mid;
   }
-  return lo;
+  return __builtin_amdgcn_readfirstlane(lo);
 }
 
 template <bool kBF16>
 __device__ __forceinline__ void store4(void* y, size_t at, f32x4 v) {
   if constexpr (kBF16) {
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + at) =
-        uint2{bf16_rne(v[0]) | (bf16_rne(v[1]) << 16), bf16_rne(v[2]) | (bf16_rne(v[3]) << 16)};
+        uint2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
   } else {
     *reinterpret_cast<f32x4*>(static_cast<float*>(y) + at) = v;
   }
+}
+
+// Outputs [at, at + 8) of a row, as many as are left (a multiple of 4).
+template <bool kBF16>
+__device__ __forceinline__ void store8_of(void* y, size_t at, int left, f32x4 v, f32x4 u) {
+  if constexpr (kBF16) {
+    if (left >= 8)
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + at) =
+          uint4{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(u[0], u[1]),
+                bf16x2_rne(u[2], u[3])};
+  } else {
+    if (left >= 4) store4<false>(y, at, v);
+    if (left >= 8) store4<false>(y, at + 4, u);
+  }
+}
+
+// Waits until this wave's LDS reads are done and at most N of its memory
+// operations (copies to LDS, stores) are outstanding, oldest first, then for
+// the other waves.
+template <int N>
+__device__ __forceinline__ void wait_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// ---- tiles staged through LDS -----------------------------------------------
+//
+// A workgroup of four waves computes 256 outputs x BM rows (BM = 32 MT), a
+// wave 128 outputs x 16 MT rows: 8 x MT accumulators of 16 x 16. Each step
+// takes 128 elements of k: 64 bytes of every row and the dword of its four
+// scales, copied from memory into one of kSlots stages of LDS without passing
+// registers. Step s multiplies from registers while it reads step s + 1 from
+// LDS and the copies of steps s + 2 to s + 4 are in flight. The steps of a
+// workgroup's tiles form one sequence, so that a tile's first copies run
+// under the end of the tile before it.
+//
+// LDS layout of a stage: rows of 64 bytes, the 16-byte piece c of row i at
+// place c ^ swizzle(i); the copy writes 64 consecutive pieces (16 rows), so
+// the swizzle is in the piece each lane fetches. A read of one piece of 16
+// rows is then free of bank conflicts. Weight rows enter the matrix unit in
+// the order n(t, i) below, which leaves a lane 8 consecutive outputs in a
+// pair of accumulators: 16-byte bf16 stores, 64 consecutive bytes per row.
+constexpr int kSlots = 4;
+constexpr int kTileN = 256;
+constexpr int kCus = 256, kXcds = 8;
+constexpr int kGroupM = 4;  // row tiles whose columns are walked together
+
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+// Buffer descriptor of `bytes` bytes at p (wave-uniform): reads past them
+// give 0.
+__device__ __forceinline__ i32x4 buffer_of(const void* p, uint32_t bytes) {
+  const uint64_t at = reinterpret_cast<uint64_t>(p);
+  return i32x4{__builtin_amdgcn_readfirstlane((int)at),
+               __builtin_amdgcn_readfirstlane((int)(at >> 32) & 0xffff),
+               __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
+}
+
+// Copies 64 lanes' 16 or 4 bytes at buf[voff + soff] to consecutive places of
+// LDS from `to` (wave-uniform). No register is written. In assembly because
+// the compiler, for its builtin, waits for every copy in flight before the
+// next read of any LDS; the waits that order copies and reads are
+// wait_barrier's.
+__device__ __forceinline__ void copy16(i32x4 buf, lds_ptr to, uint32_t voff, uint32_t soff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               ::"s"((uint32_t)(uintptr_t)to), "v"(voff), "s"(buf), "s"(soff)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(i32x4 buf, lds_ptr to, uint32_t voff, uint32_t soff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+               ::"s"((uint32_t)(uintptr_t)to), "v"(voff), "s"(buf), "s"(soff)
+               : "memory");
+}
+
+struct Tile {
+  int m0, hi, n0, e;
+};
+
+template <bool kBF16, int MT>
+struct Stage {
+  uint8_t w[kTileN * 64];
+  uint8_t a[32 * MT * 64];
+  uint32_t ws[kTileN];
+  uint32_t as[32 * MT < 256 ? 256 : 32 * MT];
+};
+
+template <bool kBF16, int MT>
+__global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p) {
+  constexpr int BM = 32 * MT;
+  constexpr int kLoads = 4 + MT / 2 + 2;  // copies of a wave and stage
+  __shared__ Stage<kBF16, MT> stage[kSlots];
+  __shared__ int first[kMaxPlanSlots + 1];
+  __shared__ int part[kExpertThreads / 64];
+  if (p.status[0] & MB_ST_FATAL) return;
+  const int nslots = p.P * p.NS;
+  tile_table<BM>(p, nslots, first, part);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int hn = wave >> 1, hm = wave & 1;
+  const int ntn = (p.n + kTileN - 1) / kTileN;
+  const int mtiles = __builtin_amdgcn_readfirstlane(first[nslots]);
+  const int total = mtiles * ntn;
+  const int kb = p.k / 2, ks = p.k / 32, steps = p.k / 128;
+  // workgroups go round the XCDs: those of one XCD take runs of consecutive
+  // tiles, which share their rows and weights in its L2
+  const int per = gridDim.x / kXcds;
+  const int xcd = blockIdx.x % kXcds, local = blockIdx.x / kXcds;
+  auto tile_index = [&](int it) { return (it * kXcds + xcd) * per + local; };
+  auto tile_of = [&](int t) {
+    Tile o;
+    const int group = t / (kGroupM * ntn), rem = t - group * (kGroupM * ntn);
+    const int gm = min(kGroupM, mtiles - group * kGroupM);
+    const int mt = group * kGroupM + rem % gm;
+    const int j = slot_of(first, nslots, mt);
+    int lo;
+    slot_rows(p, j, lo, o.hi, o.e);
+    o.m0 = lo + (mt - __builtin_amdgcn_readfirstlane(first[j])) * BM;
+    o.n0 = rem / gm * kTileN;
+    return o;
+  };
+  if (tile_index(0) >= total) return;
+  const int tiles = (total - tile_index(0) + gridDim.x - 1) / gridDim.x;
+
+  // what a lane copies: piece (lane % 4) ^ swizzle of row lane / 4 of 16
+  const int crow = lane >> 2;
+  const uint32_t cw = crow * kb + (((lane & 3) ^ (((lane >> 3) & 1) | ((lane >> 5) & 1) << 1)) << 4);
+  const uint32_t ca = crow * kb + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+  // scale dwords go to LDS in the order they are read: a lane r finds its
+  // row of every accumulator side by side
+  const int q = wave * 64 + lane;
+  const int qw = (q >> 7) * 128 + (((q >> 1) & 3) * 32) + ((q >> 5) & 3) * 8 + (q & 1) * 4 +
+                 ((q >> 3) & 3);
+  const int qa_ = q % BM;
+  const int qa = qa_ / (16 * MT) * (16 * MT) + (qa_ % MT) * 16 + (qa_ / MT) % 16;
+
+  // the copies' place in the sequence of steps: four steps ahead of the
+  // product. Past the last tile its last step is copied again, unused, so that
+  // as many copies are in flight as the waits count on.
+  i32x4 rw, ra, rws, ras;
+  Tile next;
+  int c_slot = 0;
+  auto aim = [&](int it) {
+    next = tile_of(tile_index(it));
+    const size_t wrow = (size_t)next.e * p.n + next.n0;
+    const int nw = min(kTileN, p.n - next.n0), na = min(BM, next.hi - next.m0);
+    rw = buffer_of(p.w + wrow * kb, (uint32_t)nw * kb);
+    rws = buffer_of(p.w_scale + wrow * ks, (uint32_t)nw * ks);
+    ra = buffer_of(p.a + (size_t)next.m0 * kb, (uint32_t)na * kb);
+    ras = buffer_of(p.a_scale + (size_t)next.m0 * ks, (uint32_t)na * ks);
+  };
+  auto copy = [&](int step) {
+    Stage<kBF16, MT>& s = stage[c_slot];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      copy16(rw, (lds_ptr)(s.w + (wave * 4 + j) * 1024), cw, step * 64 + (wave * 4 + j) * 16 * kb);
+#pragma unroll
+    for (int j = 0; j < MT / 2; ++j)
+      copy16(ra, (lds_ptr)(s.a + (wave * (MT / 2) + j) * 1024), ca,
+             step * 64 + (wave * (MT / 2) + j) * 16 * kb);
+    copy4(rws, (lds_ptr)(s.ws + wave * 64), qw * ks, step * 4);
+    copy4(ras, (lds_ptr)(s.as + wave * 64), qa * ks, step * 4);
+    c_slot = (c_slot + 1) & (kSlots - 1);
+  };
+
+  // Operands of the matrix unit. Each register is read from LDS for the next
+  // step as soon as its last product of this one is issued: the rows in two
+  // halves, the weights along the second half.
+  constexpr int MH = MT / 2;
+  i32x4 fw[8], fa[MT];
+  int sw[8], sa[MT];
+  const int ow = hn * 128 * 64 + ((r >> 2) * 8 + (r & 3)) * 64 +
+                 ((g ^ (((r >> 1) & 1) | ((r >> 2) & 1) << 1)) << 4);
+  const int oa = hm * 16 * MT * 64 + r * 64 + ((g ^ ((r >> 1) & 3)) << 4);
+  auto read_w = [&](int slot, int t) {
+    fw[t] = *reinterpret_cast<const i32x4*>(stage[slot].w + ow +
+                                            ((t >> 1) * 32 + (t & 1) * 4) * 64);
+  };
+  auto read_w_scales = [&](int slot, int t) {  // of four accumulators
+    const i32x4 d = *reinterpret_cast<const i32x4*>(stage[slot].ws + hn * 128 + r * 8 + t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sw[t + i] = (uint32_t)d[i] >> (8 * g);
+  };
+  auto read_a = [&](int slot, int half) {
+    const Stage<kBF16, MT>& s = stage[slot];
+#pragma unroll
+    for (int t = half * MH; t < half * MH + MH; ++t)
+      fa[t] = *reinterpret_cast<const i32x4*>(s.a + oa + t * 1024);
+    const uint32_t* d = s.as + hm * 16 * MT + r * MT + half * MH;
+#pragma unroll
+    for (int t = 0; t < MH; ++t) sa[half * MH + t] = d[t] >> (8 * g);
+  };
+
+  aim(0);
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s) copy(s);
+  wait_barrier<(kSlots - 1) * kLoads>();
+  int slot = 0, ahead = kSlots;
+#pragma unroll
+  for (int t = 0; t < 8; ++t) read_w(0, t);
+  read_w_scales(0, 0);
+  read_w_scales(0, 4);
+  read_a(0, 0);
+  for (int it = 0; it < tiles; ++it) {
+    f32x4 acc[8][MT] = {};
+    auto step = [&](int ahead) {
+      read_a(slot, 1);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int j = 0; j < MH; ++j)
+          acc[i][j] = mfma_mx4(fw[i], fa[j], acc[i][j], sw[i], sa[j]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // this wave's reads of the slot are done, and its copies of the next
+      // step have landed; after the barrier that holds for all waves
+      wait_barrier<(kSlots - 2) * kLoads>();
+      copy(ahead);  // into the slot just read
+      slot = (slot + 1) & (kSlots - 1);
+      read_a(slot, 0);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int j = MH; j < MT; ++j)
+          acc[i][j] = mfma_mx4(fw[i], fa[j], acc[i][j], sw[i], sa[j]);
+        read_w(slot, i);
+        if (i % 4 == 3) read_w_scales(slot, i - 3);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    Tile tile = next;
+    for (int s = 0; s < steps; ++s) {
+      if (ahead == steps) {  // four steps before the tile's end
+        tile = next;
+        ahead = steps - 1;
+        if (it + 1 < tiles) {
+          aim(it + 1);
+          ahead = 0;
+        }
+      }
+      step(ahead++);
+    }
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+      const int m = tile.m0 + (hm * MT + j) * 16 + r;
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const int nn = tile.n0 + hn * 128 + (i >> 1) * 32 + g * 8;
+        if (m < tile.hi)
+          store8_of<kBF16>(p.y, (size_t)m * p.n + nn, p.n - nn, acc[i][j], acc[i + 1][j]);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // one row of accumulators at a time: no spills
+    }
+  }
+  // no copy may reach LDS after the workgroup has given it back
+  wait_barrier<0>();
 }
 
 // 64 x 64 tiles, operands straight from memory: wave w holds 16 outputs of
@@ -155,6 +415,21 @@ hipError_t launch_expert_mx4(const mb_dims& d, const Geometry& g, const mb_plan_
   const ExpertArgs p = {a,         a_scale, w,           w_scale, y,
                         o.cu_seqlens, o.rep_expert, o.status, d.n_ranks, d.n_experts,
                         g.Eh,      g.NS,    d.slots_per_rank, d.cap, n_out, k_in};
+  const int64_t rows = (int64_t)d.n_tokens * d.top_k;
+  if (k_in >= 128 * kSlots && rows >= (int64_t)d.n_ranks * g.NS * 128) {
+    if (d.dtype_out == MB_BF16)
+      hipLaunchKernelGGL((k_expert_tile<true, 8>), dim3(kCus), dim3(kExpertThreads), 0, st, p);
+    else
+      hipLaunchKernelGGL((k_expert_tile<false, 8>), dim3(kCus), dim3(kExpertThreads), 0, st, p);
+    return hipGetLastError();
+  }
+  if (k_in >= 128 * kSlots && rows >= (int64_t)d.n_ranks * g.NS * 32) {
+    if (d.dtype_out == MB_BF16)
+      hipLaunchKernelGGL((k_expert_tile<true, 4>), dim3(kCus), dim3(kExpertThreads), 0, st, p);
+    else
+      hipLaunchKernelGGL((k_expert_tile<false, 4>), dim3(kCus), dim3(kExpertThreads), 0, st, p);
+    return hipGetLastError();
+  }
   const int grid = 1024;
   if (d.dtype_out == MB_BF16)
     hipLaunchKernelGGL(k_expert_mx4<true>, dim3(grid), dim3(kExpertThreads), 0, st, p);

@@ -7,11 +7,15 @@
 
 namespace mb {
 
-// fp32 to bf16, round to nearest even, NaN kept quiet.
-__device__ __forceinline__ uint32_t bf16_rne(float f) {
-  const uint32_t b = __float_as_uint(f);
-  if ((b & 0x7fffffffu) > 0x7f800000u) return (b >> 16) | 0x40u;
-  return (b + 0x7fffu + ((b >> 16) & 1u)) >> 16;
+// Two fp32 values to packed bf16, round to nearest even (v_cvt_pk_bf16_f32).
+__device__ __forceinline__ uint32_t bf16x2_rne(float a, float b) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const f32x2 v = {a, b};
+  const bf16x2 o = __builtin_convertvector(v, bf16x2);
+  uint32_t u;
+  __builtin_memcpy(&u, &o, 4);
+  return u;
 }
 
 // v[0..8) = elements [8c, 8c + 8) of p.
@@ -37,7 +41,7 @@ __device__ __forceinline__ void store8(void* p, size_t c, const float* v) {
   if constexpr (kBF16) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = bf16_rne(v[2 * i]) | (bf16_rne(v[2 * i + 1]) << 16);
+    for (int i = 0; i < 4; ++i) w[i] = bf16x2_rne(v[2 * i], v[2 * i + 1]);
     static_cast<uint4*>(p)[c] = uint4{w[0], w[1], w[2], w[3]};
   } else {
     static_cast<float4*>(p)[2 * c] = float4{v[0], v[1], v[2], v[3]};
