@@ -129,29 +129,34 @@ __device__ __forceinline__ void wait_barrier() {
 // ---- tiles staged through LDS -----------------------------------------------
 //
 // A workgroup of four waves computes 256 outputs x BM rows (BM = 32 MT), a
-// wave 128 outputs x 16 MT rows: 8 x MT accumulators of 16 x 16. Each step
-// takes 128 elements of k: 64 bytes of every row and the dword of its four
-// scales, copied from memory into one of kSlots stages of LDS without passing
-// registers. Step s multiplies from registers while it reads step s + 1 from
-// LDS and the copies of steps s + 2 to s + 4 are in flight. The steps of a
-// workgroup's tiles form one sequence, so that a tile's first copies run
-// under the end of the tile before it.
+// wave 128 outputs x 16 MT rows: 8 x MT accumulators of 16 x 16. A step takes
+// 128 elements of k. Rows are copied from memory into LDS, without passing
+// registers, in pairs of steps: 128 bytes of every row, one cache line. (With
+// single steps, 64 bytes of a row and 4 of its scales at a time, the L2's
+// requests set the pace: 10.5 ms for 1048576 rows of 7168 by 2048, twice the
+// requests for rows and eight times those for scales.) The scales are copied
+// in groups of four steps, 16 bytes of every row. Two pairs and two groups
+// are in LDS; the pair two ahead is copied as soon as the last operand of the
+// present one is in registers. The pairs of a workgroup's tiles form one
+// sequence, so that a tile's first copies run under the end of the tile
+// before it.
 //
-// LDS layout of a stage: rows of 64 bytes, the 16-byte piece c of row i at
-// place c ^ swizzle(i); the copy writes 64 consecutive pieces (16 rows), so
-// the swizzle is in the piece each lane fetches. A read of one piece of 16
-// rows is then free of bank conflicts. Weight rows enter the matrix unit in
-// the order n(t, i) below, which leaves a lane 8 consecutive outputs in a
-// pair of accumulators: 16-byte bf16 stores, 64 consecutive bytes per row.
-constexpr int kSlots = 4;
+// LDS layout of a pair: rows of 128 bytes, the 16-byte piece c of a row at
+// place c ^ swizzle; the copy writes 64 consecutive pieces (8 rows), so the
+// swizzle is in the piece each lane fetches. A read of one piece of 16 rows
+// then meets every bank once. Weight rows enter the matrix unit in the order
+// n(t, i) = (t / 2) 32 + (i / 4) 8 + (t % 2) 4 + i % 4 (accumulator t, row i),
+// which leaves a lane 8 consecutive outputs in two accumulators: 16-byte
+// bf16 stores, 64 consecutive bytes per row.
 constexpr int kTileN = 256;
 constexpr int kCus = 256, kXcds = 8;
 constexpr int kGroupM = 4;  // row tiles whose columns are walked together
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
 
-// Buffer descriptor of `bytes` bytes at p (wave-uniform): reads past them
-// give 0.
+// Buffer descriptor of `bytes` bytes at p (wave-uniform). A read at voff +
+// soff gives 0 where voff >= bytes - soff: soff must be below bytes, so what
+// may pass the end is always in voff.
 __device__ __forceinline__ i32x4 buffer_of(const void* p, uint32_t bytes) {
   const uint64_t at = reinterpret_cast<uint64_t>(p);
   return i32x4{__builtin_amdgcn_readfirstlane((int)at),
@@ -169,41 +174,40 @@ __device__ __forceinline__ void copy16(i32x4 buf, lds_ptr to, uint32_t voff, uin
                ::"s"((uint32_t)(uintptr_t)to), "v"(voff), "s"(buf), "s"(soff)
                : "memory");
 }
-__device__ __forceinline__ void copy4(i32x4 buf, lds_ptr to, uint32_t voff, uint32_t soff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
-               ::"s"((uint32_t)(uintptr_t)to), "v"(voff), "s"(buf), "s"(soff)
-               : "memory");
+__device__ __forceinline__ i32x4 piece_at(const uint8_t* p) {
+  return *static_cast<const i32x4*>(__builtin_assume_aligned(p, 16));
 }
 
 struct Tile {
   int m0, hi, n0, e;
 };
 
-template <bool kBF16, int MT>
-struct Stage {
-  uint8_t w[kTileN * 64];
-  uint8_t a[32 * MT * 64];
-  uint32_t ws[kTileN];
-  uint32_t as[32 * MT < 256 ? 256 : 32 * MT];
+template <int MT>
+struct alignas(16) TileLds {
+  uint8_t w[2][kTileN * 128];
+  uint8_t a[2][32 * MT * 128];
+  uint8_t ws[2][kTileN * 16];
+  uint8_t as[2][kTileN * 16];  // 32 MT rows, copied by four waves: twice over when MT = 4
+  uint8_t none[4 * 1024];      // where copies of nothing go
+  int first[kMaxPlanSlots + 1];
+  int part[kExpertThreads / 64];
 };
 
 template <bool kBF16, int MT>
 __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p) {
-  constexpr int BM = 32 * MT;
-  constexpr int kLoads = 4 + MT / 2 + 2;  // copies of a wave and stage
-  __shared__ Stage<kBF16, MT> stage[kSlots];
-  __shared__ int first[kMaxPlanSlots + 1];
-  __shared__ int part[kExpertThreads / 64];
+  constexpr int BM = 32 * MT, MH = MT / 2;
+  __shared__ TileLds<MT> lds;
   if (p.status[0] & MB_ST_FATAL) return;
   const int nslots = p.P * p.NS;
-  tile_table<BM>(p, nslots, first, part);
+  tile_table<BM>(p, nslots, lds.first, lds.part);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int hn = wave >> 1, hm = wave & 1;
   const int ntn = (p.n + kTileN - 1) / kTileN;
-  const int mtiles = __builtin_amdgcn_readfirstlane(first[nslots]);
+  const int mtiles = __builtin_amdgcn_readfirstlane(lds.first[nslots]);
   const int total = mtiles * ntn;
   const int kb = p.k / 2, ks = p.k / 32, steps = p.k / 128;
+  const int pairs = (steps + 1) / 2;
   // workgroups go round the XCDs: those of one XCD take runs of consecutive
   // tiles, which share their rows and weights in its L2
   const int per = gridDim.x / kXcds;
@@ -214,34 +218,36 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
     const int group = t / (kGroupM * ntn), rem = t - group * (kGroupM * ntn);
     const int gm = min(kGroupM, mtiles - group * kGroupM);
     const int mt = group * kGroupM + rem % gm;
-    const int j = slot_of(first, nslots, mt);
+    const int j = slot_of(lds.first, nslots, mt);
     int lo;
     slot_rows(p, j, lo, o.hi, o.e);
-    o.m0 = lo + (mt - __builtin_amdgcn_readfirstlane(first[j])) * BM;
+    o.m0 = lo + (mt - __builtin_amdgcn_readfirstlane(lds.first[j])) * BM;
     o.n0 = rem / gm * kTileN;
     return o;
   };
   if (tile_index(0) >= total) return;
   const int tiles = (total - tile_index(0) + gridDim.x - 1) / gridDim.x;
 
-  // what a lane copies: piece (lane % 4) ^ swizzle of row lane / 4 of 16
-  const int crow = lane >> 2;
-  const uint32_t cw = crow * kb + (((lane & 3) ^ (((lane >> 3) & 1) | ((lane >> 5) & 1) << 1)) << 4);
-  const uint32_t ca = crow * kb + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
-  // scale dwords go to LDS in the order they are read: a lane r finds its
-  // row of every accumulator side by side
-  const int q = wave * 64 + lane;
-  const int qw = (q >> 7) * 128 + (((q >> 1) & 3) * 32) + ((q >> 5) & 3) * 8 + (q & 1) * 4 +
-                 ((q >> 3) & 3);
-  const int qa_ = q % BM;
-  const int qa = qa_ / (16 * MT) * (16 * MT) + (qa_ % MT) * 16 + (qa_ / MT) % 16;
+  // What a lane copies: of 8 rows, piece (lane % 8) ^ swizzle of row lane / 8.
+  // The swizzle of row i of 16 in the matrix unit is i / 2; blocks of 8 rows
+  // differ in it by constants.
+  const int crow = lane >> 3;
+  uint32_t ca[2], cw[4];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) ca[j] = crow * kb + (((lane & 7) ^ (crow >> 1) ^ (j << 2)) << 4);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    cw[j] = crow * kb + (((lane & 7) ^ ((crow >> 1) & 1) ^ (j << 1)) << 4);
+  // scales: lane = row, in the order of the accumulators' rows
+  const int q = wave * 64 + lane, qi = q & 15, qt = (q >> 4) & 7;
+  const uint32_t csw = ((q >> 7) * 128 + (qt >> 1) * 32 + (qi >> 2) * 8 + (qt & 1) * 4 + (qi & 3)) * ks;
+  const uint32_t csa = (q % BM) * ks;
 
-  // the copies' place in the sequence of steps: four steps ahead of the
-  // product. Past the last tile its last step is copied again, unused, so that
-  // as many copies are in flight as the waits count on.
+  // the copies' place in the sequence of pairs: two ahead of the product.
+  // Past the last tile its last pair is copied again, unused.
   i32x4 rw, ra, rws, ras;
   Tile next;
-  int c_slot = 0;
+  int c_buf = 0, c_group = 0;
   auto aim = [&](int it) {
     next = tile_of(tile_index(it));
     const size_t wrow = (size_t)next.e * p.n + next.n0;
@@ -251,97 +257,98 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
     ra = buffer_of(p.a + (size_t)next.m0 * kb, (uint32_t)na * kb);
     ras = buffer_of(p.a_scale + (size_t)next.m0 * ks, (uint32_t)na * ks);
   };
-  auto copy = [&](int step) {
-    Stage<kBF16, MT>& s = stage[c_slot];
+  auto copy = [&](int pair) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      copy16(rw, (lds_ptr)(s.w + (wave * 4 + j) * 1024), cw, step * 64 + (wave * 4 + j) * 16 * kb);
+    for (int j = 0; j < 8; ++j)
+      copy16(rw, (lds_ptr)(lds.w[c_buf] + (wave * 8 + j) * 1024),
+             cw[j & 3] + (wave * 8 + j) * 8 * kb, pair * 128);
 #pragma unroll
-    for (int j = 0; j < MT / 2; ++j)
-      copy16(ra, (lds_ptr)(s.a + (wave * (MT / 2) + j) * 1024), ca,
-             step * 64 + (wave * (MT / 2) + j) * 16 * kb);
-    copy4(rws, (lds_ptr)(s.ws + wave * 64), qw * ks, step * 4);
-    copy4(ras, (lds_ptr)(s.as + wave * 64), qa * ks, step * 4);
-    c_slot = (c_slot + 1) & (kSlots - 1);
+    for (int j = 0; j < MT; ++j)
+      copy16(ra, (lds_ptr)(lds.a[c_buf] + (wave * MT + j) * 1024),
+             ca[j & 1] + (wave * MT + j) * 8 * kb, pair * 128);
+    // the scales of this pair and the next; nothing in the second of a group
+    const bool group = !(pair & 1);
+    c_group ^= group ? 1 : 0;
+    const uint32_t none = group ? 0u : 0x80000000u;
+    copy16(rws, (lds_ptr)((group ? lds.ws[c_group] : lds.none) + wave * 1024), csw | none,
+           (pair >> 1) * 16);
+    copy16(ras, (lds_ptr)((group ? lds.as[c_group] : lds.none) + wave * 1024), csa | none,
+           (pair >> 1) * 16);
+    c_buf ^= 1;
   };
 
   // Operands of the matrix unit. Each register is read from LDS for the next
   // step as soon as its last product of this one is issued: the rows in two
   // halves, the weights along the second half.
-  constexpr int MH = MT / 2;
   i32x4 fw[8], fa[MT];
   int sw[8], sa[MT];
-  const int ow = hn * 128 * 64 + ((r >> 2) * 8 + (r & 3)) * 64 +
-                 ((g ^ (((r >> 1) & 1) | ((r >> 2) & 1) << 1)) << 4);
-  const int oa = hm * 16 * MT * 64 + r * 64 + ((g ^ ((r >> 1) & 3)) << 4);
-  auto read_w = [&](int slot, int t) {
-    fw[t] = *reinterpret_cast<const i32x4*>(stage[slot].w + ow +
-                                            ((t >> 1) * 32 + (t & 1) * 4) * 64);
+  const int ow = (hn * 128 + (r >> 2) * 8 + (r & 3)) * 128, oa = (hm * 16 * MT + r) * 128;
+  const int piece = (g ^ (r >> 1)) << 4;  // of the first step of a pair; the second's is piece ^ 64
+  auto read_w = [&](int buf, int half, int t) {
+    fw[t] = piece_at(lds.w[buf] + ow + (piece ^ half * 64) + ((t >> 1) * 32 + (t & 1) * 4) * 128);
   };
-  auto read_w_scales = [&](int slot, int t) {  // of four accumulators
-    const i32x4 d = *reinterpret_cast<const i32x4*>(stage[slot].ws + hn * 128 + r * 8 + t);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sw[t + i] = (uint32_t)d[i] >> (8 * g);
+  auto read_a = [&](int buf, int half, int t) {
+    fa[t] = piece_at(lds.a[buf] + oa + (piece ^ half * 64) + t * 16 * 128);
   };
-  auto read_a = [&](int slot, int half) {
-    const Stage<kBF16, MT>& s = stage[slot];
-#pragma unroll
-    for (int t = half * MH; t < half * MH + MH; ++t)
-      fa[t] = *reinterpret_cast<const i32x4*>(s.a + oa + t * 1024);
-    const uint32_t* d = s.as + hm * 16 * MT + r * MT + half * MH;
-#pragma unroll
-    for (int t = 0; t < MH; ++t) sa[half * MH + t] = d[t] >> (8 * g);
+  auto scale = [&](const uint8_t* s, int row, int step) {
+    return (int)s[(row + r) * 16 + (step & 3) * 4 + g];
   };
 
   aim(0);
+  c_group = 1;
+  copy(0);
+  copy(1);
+  wait_barrier<0>();
+  int buf = 0, grp = 0, ahead = 2;
 #pragma unroll
-  for (int s = 0; s < kSlots; ++s) copy(s);
-  wait_barrier<(kSlots - 1) * kLoads>();
-  int slot = 0, ahead = kSlots;
+  for (int t = 0; t < 8; ++t) read_w(0, 0, t), sw[t] = scale(lds.ws[0], hn * 128 + t * 16, 0);
 #pragma unroll
-  for (int t = 0; t < 8; ++t) read_w(0, t);
-  read_w_scales(0, 0);
-  read_w_scales(0, 4);
-  read_a(0, 0);
+  for (int t = 0; t < MH; ++t) read_a(0, 0, t), sa[t] = scale(lds.as[0], (hm * MT + t) * 16, 0);
   for (int it = 0; it < tiles; ++it) {
     f32x4 acc[8][MT] = {};
-    auto step = [&](int ahead) {
-      read_a(slot, 1);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-#pragma unroll
-        for (int j = 0; j < MH; ++j)
-          acc[i][j] = mfma_mx4(fw[i], fa[j], acc[i][j], sw[i], sa[j]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      // this wave's reads of the slot are done, and its copies of the next
-      // step have landed; after the barrier that holds for all waves
-      wait_barrier<(kSlots - 2) * kLoads>();
-      copy(ahead);  // into the slot just read
-      slot = (slot + 1) & (kSlots - 1);
-      read_a(slot, 0);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-#pragma unroll
-        for (int j = MH; j < MT; ++j)
-          acc[i][j] = mfma_mx4(fw[i], fa[j], acc[i][j], sw[i], sa[j]);
-        read_w(slot, i);
-        if (i % 4 == 3) read_w_scales(slot, i - 3);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    };
     Tile tile = next;
     for (int s = 0; s < steps; ++s) {
-      if (ahead == steps) {  // four steps before the tile's end
+      if (ahead == pairs) {  // at the end of the last pair but two
         tile = next;
-        ahead = steps - 1;
+        ahead = pairs - 1;
         if (it + 1 < tiles) {
           aim(it + 1);
           ahead = 0;
         }
       }
-      step(ahead++);
+      // the second half of this step's rows is read under the products of the
+      // first half
+#pragma unroll
+      for (int t = MH; t < MT; ++t)
+        read_a(buf, s & 1, t), sa[t] = scale(lds.as[grp], (hm * MT + t) * 16, s);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int j = 0; j < MH; ++j) acc[i][j] = mfma_mx4(fw[i], fa[j], acc[i][j], sw[i], sa[j]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      const int step = s + 1 < steps ? s + 1 : 0;  // the next
+      if (!(step & 1)) {
+        // this wave has read all of the pair, and its copies of the next have
+        // landed; after the barrier that holds for all waves
+        wait_barrier<0>();
+        copy(ahead++);
+        buf ^= 1;
+        grp ^= step & 2 ? 0 : 1;
+      }
+      // the next step's operands, under the products of the second half
+#pragma unroll
+      for (int t = 0; t < MH; ++t)
+        read_a(buf, step & 1, t), sa[t] = scale(lds.as[grp], (hm * MT + t) * 16, step);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int j = MH; j < MT; ++j) acc[i][j] = mfma_mx4(fw[i], fa[j], acc[i][j], sw[i], sa[j]);
+        read_w(buf, step & 1, i), sw[i] = scale(lds.ws[grp], hn * 128 + i * 16, step);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
@@ -416,14 +423,14 @@ hipError_t launch_expert_mx4(const mb_dims& d, const Geometry& g, const mb_plan_
                         o.cu_seqlens, o.rep_expert, o.status, d.n_ranks, d.n_experts,
                         g.Eh,      g.NS,    d.slots_per_rank, d.cap, n_out, k_in};
   const int64_t rows = (int64_t)d.n_tokens * d.top_k;
-  if (k_in >= 128 * kSlots && rows >= (int64_t)d.n_ranks * g.NS * 128) {
+  if (k_in >= 384 && rows >= (int64_t)d.n_ranks * g.NS * 128) {
     if (d.dtype_out == MB_BF16)
       hipLaunchKernelGGL((k_expert_tile<true, 8>), dim3(kCus), dim3(kExpertThreads), 0, st, p);
     else
       hipLaunchKernelGGL((k_expert_tile<false, 8>), dim3(kCus), dim3(kExpertThreads), 0, st, p);
     return hipGetLastError();
   }
-  if (k_in >= 128 * kSlots && rows >= (int64_t)d.n_ranks * g.NS * 32) {
+  if (k_in >= 384 && rows >= (int64_t)d.n_ranks * g.NS * 32) {
     if (d.dtype_out == MB_BF16)
       hipLaunchKernelGGL((k_expert_tile<true, 4>), dim3(kCus), dim3(kExpertThreads), 0, st, p);
     else
