@@ -19,6 +19,7 @@ namespace {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kExpertThreads = 256;
 constexpr int kMaxPlanSlots = kMaxExperts + kMaxRanks * kMaxSlots;
@@ -42,6 +43,14 @@ __device__ __forceinline__ f32x4 mfma_mx4(i32x4 a, i32x4 b, f32x4 c, int sa, int
 }
 
 typedef const __attribute__((address_space(4))) int32_t* plan_ptr;
+
+// u: which byte of the lanes' scales (the builtin takes it as a constant).
+__device__ __forceinline__ f32x16 mfma_mx4(i32x4 a, i32x4 b, f32x16 c, int sa, int sb, int u) {
+  const i32x8 a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0};
+  const i32x8 b8 = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
+  return u ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, 1, sa, 1, sb)
+           : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, 0, sa, 0, sb);
+}
 
 // Rows [lo, hi) of slot j (r = j / NS), absolute in the buffer, and its
 // expert; empty when it holds none. Only a broken plan needs the clamps.
@@ -128,26 +137,29 @@ __device__ __forceinline__ void wait_barrier() {
 
 // ---- tiles staged through LDS -----------------------------------------------
 //
-// A workgroup of four waves computes 256 outputs x BM rows (BM = 32 MT), a
-// wave 128 outputs x 16 MT rows: 8 x MT accumulators of 16 x 16. A step takes
-// 128 elements of k. Rows are copied from memory into LDS, without passing
-// registers, in pairs of steps: 128 bytes of every row, one cache line. (With
-// single steps, 64 bytes of a row and 4 of its scales at a time, the L2's
-// requests set the pace: 10.5 ms for 1048576 rows of 7168 by 2048, twice the
-// requests for rows and eight times those for scales.) The scales are copied
-// in groups of four steps, 16 bytes of every row. Two pairs and two groups
-// are in LDS; the pair two ahead is copied as soon as the last operand of the
-// present one is in registers. The pairs of a workgroup's tiles form one
-// sequence, so that a tile's first copies run under the end of the tile
-// before it.
+// A workgroup of four waves computes 256 outputs x BM rows (BM = 64 JT), a
+// wave 128 outputs x 32 JT rows: 4 x JT accumulators of 32 x 32 by
+// v_mfma_scale_f32_32x32x64_f8f6f4 (lane r = lane % 32 of an operand's rows,
+// h = lane / 32 of its two blocks of 32 elements; outputs 8a + 4h + b of row
+// r at accumulator 4a + b).
+//
+// A step takes 128 elements of k. Rows are copied from memory into LDS,
+// without passing registers, in pairs of steps: 128 bytes of every row, one
+// cache line. (With single steps, 64 bytes of a row and 4 of its scales at a
+// time, the L2's requests set the pace.) The scales are copied in groups of
+// four steps, 16 bytes of every row. Two pairs and two groups are in LDS; the
+// pair two ahead is copied as soon as the last operand of the present one is
+// in registers. The pairs of a workgroup's tiles form one sequence, so that a
+// tile's first copies run under the end of the tile before it.
 //
 // LDS layout of a pair: rows of 128 bytes, the 16-byte piece c of a row at
 // place c ^ swizzle; the copy writes 64 consecutive pieces (8 rows), so the
-// swizzle is in the piece each lane fetches. A read of one piece of 16 rows
-// then meets every bank once. Weight rows enter the matrix unit in the order
-// n(t, i) = (t / 2) 32 + (i / 4) 8 + (t % 2) 4 + i % 4 (accumulator t, row i),
-// which leaves a lane 8 consecutive outputs in two accumulators: 16-byte
-// bf16 stores, 64 consecutive bytes per row.
+// swizzle is in the piece each lane fetches. A read of one piece of 32 rows
+// then meets every bank once in 16 lanes. Block (step, h, u) of a pair, u the
+// product of the step, is piece 4 step + 2 h + u: a lane's two scales of a
+// step are then neighbours. Weight row n enters the matrix unit as row
+// swap23(n % 32), bits 2 and 3 exchanged, which leaves a lane 8 consecutive
+// outputs in 8 consecutive accumulators: 16-byte bf16 stores.
 constexpr int kTileN = 256;
 constexpr int kCus = 256, kXcds = 8;
 constexpr int kGroupM = 4;  // row tiles whose columns are walked together
@@ -182,26 +194,27 @@ struct Tile {
   int m0, hi, n0, e;
 };
 
-template <int MT>
+template <int JT>
 struct alignas(16) TileLds {
   uint8_t w[2][kTileN * 128];
-  uint8_t a[2][32 * MT * 128];
+  uint8_t a[2][64 * JT * 128];
   uint8_t ws[2][kTileN * 16];
-  uint8_t as[2][kTileN * 16];  // 32 MT rows, copied by four waves: twice over when MT = 4
-  uint8_t none[4 * 1024];      // where copies of nothing go
+  uint8_t as[2][kTileN * 16];  // 64 JT rows, copied by four waves: twice over when JT = 2
+  uint8_t none[kTileN * 16];   // zeros: where copies of nothing go, the scales behind a row
   int first[kMaxPlanSlots + 1];
   int part[kExpertThreads / 64];
 };
 
-template <bool kBF16, int MT>
+template <bool kBF16, int JT>
 __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p) {
-  constexpr int BM = 32 * MT, MH = MT / 2;
-  __shared__ TileLds<MT> lds;
+  constexpr int BM = 64 * JT, JH = JT / 2;
+  __shared__ TileLds<JT> lds;
   if (p.status[0] & MB_ST_FATAL) return;
   const int nslots = p.P * p.NS;
+  reinterpret_cast<uint4*>(lds.none)[threadIdx.x] = uint4{};
   tile_table<BM>(p, nslots, lds.first, lds.part);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15, g = lane >> 4;
+  const int r = lane & 31, h = lane >> 5;
   const int hn = wave >> 1, hm = wave & 1;
   const int ntn = (p.n + kTileN - 1) / kTileN;
   const int mtiles = __builtin_amdgcn_readfirstlane(lds.first[nslots]);
@@ -228,26 +241,25 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
   if (tile_index(0) >= total) return;
   const int tiles = (total - tile_index(0) + gridDim.x - 1) / gridDim.x;
 
-  // What a lane copies: of 8 rows, piece (lane % 8) ^ swizzle of row lane / 8.
-  // The swizzle of row i of 16 in the matrix unit is i / 2; blocks of 8 rows
-  // differ in it by constants.
+  // What a lane copies: of 8 rows, piece (lane % 8) ^ swizzle of row crow.
+  // The swizzle of matrix-unit row i is i / 2 % 8; blocks of 8 rows differ in
+  // it by constants. cut: its lanes whose piece lies in the second step.
   const int crow = lane >> 3;
-  uint32_t ca[2], cw[4];
+  uint32_t ca[2], cw[2], cut_a[2];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) ca[j] = crow * kb + (((lane & 7) ^ (crow >> 1) ^ (j << 2)) << 4);
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    cw[j] = crow * kb + (((lane & 7) ^ ((crow >> 1) & 1) ^ (j << 1)) << 4);
-  // scales: lane = row, in the order of the accumulators' rows
-  const int q = wave * 64 + lane, qi = q & 15, qt = (q >> 4) & 7;
-  const uint32_t csw = ((q >> 7) * 128 + (qt >> 1) * 32 + (qi >> 2) * 8 + (qt & 1) * 4 + (qi & 3)) * ks;
-  const uint32_t csa = (q % BM) * ks;
+  for (int j = 0; j < 2; ++j) {
+    ca[j] = crow * kb + (((lane & 7) ^ (crow >> 1) ^ (j << 2)) << 4);
+    cw[j] = crow * kb + (((lane & 7) ^ (((crow >> 1) & 1) | (crow & 4)) ^ (j << 1)) << 4);
+    cut_a[j] = ((lane ^ (j << 2)) & 4) ? 0x80000000u : 0u;
+  }
+  const uint32_t cut_w = ((lane ^ crow) & 4) ? 0x80000000u : 0u;
+  const uint32_t csw = (wave * 64 + lane) * ks, csa = (wave * 64 + lane) % BM * ks;
 
   // the copies' place in the sequence of pairs: two ahead of the product.
   // Past the last tile its last pair is copied again, unused.
   i32x4 rw, ra, rws, ras;
   Tile next;
-  int c_buf = 0, c_group = 0;
+  int c_buf = 0, c_group = 1;
   auto aim = [&](int it) {
     next = tile_of(tile_index(it));
     const size_t wrow = (size_t)next.e * p.n + next.n0;
@@ -257,57 +269,77 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
     ra = buffer_of(p.a + (size_t)next.m0 * kb, (uint32_t)na * kb);
     ras = buffer_of(p.a_scale + (size_t)next.m0 * ks, (uint32_t)na * ks);
   };
-  auto copy = [&](int pair) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      copy16(rw, (lds_ptr)(lds.w[c_buf] + (wave * 8 + j) * 1024),
-             cw[j & 3] + (wave * 8 + j) * 8 * kb, pair * 128);
-#pragma unroll
-    for (int j = 0; j < MT; ++j)
-      copy16(ra, (lds_ptr)(lds.a[c_buf] + (wave * MT + j) * 1024),
-             ca[j & 1] + (wave * MT + j) * 8 * kb, pair * 128);
-    // the scales of this pair and the next; nothing in the second of a group
-    const bool group = !(pair & 1);
-    c_group ^= group ? 1 : 0;
-    const uint32_t none = group ? 0u : 0x80000000u;
-    copy16(rws, (lds_ptr)((group ? lds.ws[c_group] : lds.none) + wave * 1024), csw | none,
-           (pair >> 1) * 16);
-    copy16(ras, (lds_ptr)((group ? lds.as[c_group] : lds.none) + wave * 1024), csa | none,
-           (pair >> 1) * 16);
-    c_buf ^= 1;
+  // Copy c of the kCopies of a pair. With an odd number of steps the second
+  // half of the last pair lies behind the row: its lanes read out of range,
+  // zeros.
+  constexpr int kCopies = 8 + 2 * JT + 2;
+  auto copy = [&](int pair, int c) {
+    const uint32_t last = 2 * pair + 1 == steps ? 0x80000000u : 0u;
+    if (c < 8) {
+      copy16(rw, (lds_ptr)(lds.w[c_buf] + (wave * 8 + c) * 1024),
+             (cw[c & 1] + (wave * 8 + c) * 8 * kb) | (cut_w & last), pair * 128);
+    } else if (c < 8 + 2 * JT) {
+      const int j = c - 8;
+      copy16(ra, (lds_ptr)(lds.a[c_buf] + (wave * 2 * JT + j) * 1024),
+             (ca[j & 1] + (wave * 2 * JT + j) * 8 * kb) | (cut_a[j & 1] & last), pair * 128);
+    } else {
+      // the scales of this pair and the next; nothing in the second of a group
+      const bool group = !(pair & 1);
+      const uint32_t none = group ? 0u : 0x80000000u;
+      if (c == 8 + 2 * JT) {
+        c_group ^= group ? 1 : 0;
+        copy16(rws, (lds_ptr)((group ? lds.ws[c_group] : lds.none) + wave * 1024), csw | none,
+               (pair >> 1) * 16);
+      } else {
+        copy16(ras, (lds_ptr)((group ? lds.as[c_group] : lds.none) + wave * 1024), csa | none,
+               (pair >> 1) * 16);
+      }
+    }
   };
 
-  // Operands of the matrix unit. Each register is read from LDS for the next
-  // step as soon as its last product of this one is issued: the rows in two
-  // halves, the weights along the second half.
-  i32x4 fw[8], fa[MT];
-  int sw[8], sa[MT];
-  const int ow = (hn * 128 + (r >> 2) * 8 + (r & 3)) * 128, oa = (hm * 16 * MT + r) * 128;
-  const int piece = (g ^ (r >> 1)) << 4;  // of the first step of a pair; the second's is piece ^ 64
-  auto read_w = [&](int buf, int half, int t) {
-    fw[t] = piece_at(lds.w[buf] + ow + (piece ^ half * 64) + ((t >> 1) * 32 + (t & 1) * 4) * 128);
+  // Operands of the matrix unit, [accumulator][product of the step]. Each
+  // register is read from LDS for the next step as soon as its last product
+  // of this one is issued: the rows in two halves, the weights along the
+  // second half.
+  i32x4 fw[4][2], fa[JT][2];
+  int sw[4], sa[JT];
+  const int rn = (r & 19) | ((r & 4) << 1) | ((r & 8) >> 1);  // swap23
+  const int ow = (hn * 128 + rn) * 128, oa = (hm * 32 * JT + r) * 128;
+  const int piece = ((2 * h) ^ ((r >> 1) & 7)) << 4;  // of (step 0, h, 0)
+  auto read_w = [&](int buf, int step, int t, int u) {
+    fw[t][u] = piece_at(lds.w[buf] + ow + (piece ^ (step * 64 + u * 16)) + t * 32 * 128);
   };
-  auto read_a = [&](int buf, int half, int t) {
-    fa[t] = piece_at(lds.a[buf] + oa + (piece ^ half * 64) + t * 16 * 128);
+  auto read_a = [&](int buf, int step, int t, int u) {
+    fa[t][u] = piece_at(lds.a[buf] + oa + (piece ^ (step * 64 + u * 16)) + t * 32 * 128);
   };
-  auto scale = [&](const uint8_t* s, int row, int step) {
-    return (int)s[(row + r) * 16 + (step & 3) * 4 + g];
+  // the two scales of a step (0..3 of its group), all rows at s
+  auto scales = [&](const uint8_t* s, int row, int step) {
+    return (int)*reinterpret_cast<const uint16_t*>(s + row * 16 + step * 4 + 2 * h);
   };
 
   aim(0);
-  c_group = 1;
-  copy(0);
-  copy(1);
+#pragma unroll
+  for (int c = 0; c < kCopies; ++c) copy(0, c);
+  c_buf = 1;
+#pragma unroll
+  for (int c = 0; c < kCopies; ++c) copy(1, c);
+  c_buf = 0;
   wait_barrier<0>();
   int buf = 0, grp = 0, ahead = 2;
 #pragma unroll
-  for (int t = 0; t < 8; ++t) read_w(0, 0, t), sw[t] = scale(lds.ws[0], hn * 128 + t * 16, 0);
+  for (int t = 0; t < 4; ++t) {
+    read_w(0, 0, t, 0), read_w(0, 0, t, 1);
+    sw[t] = scales(lds.ws[0], hn * 128 + t * 32 + rn, 0);
+  }
 #pragma unroll
-  for (int t = 0; t < MH; ++t) read_a(0, 0, t), sa[t] = scale(lds.as[0], (hm * MT + t) * 16, 0);
+  for (int t = 0; t < JH; ++t) {
+    read_a(0, 0, t, 0), read_a(0, 0, t, 1);
+    sa[t] = scales(lds.as[0], (hm * JT + t) * 32 + r, 0);
+  }
   for (int it = 0; it < tiles; ++it) {
-    f32x4 acc[8][MT] = {};
+    f32x16 acc[4][JT] = {};
     Tile tile = next;
-    for (int s = 0; s < steps; ++s) {
+    for (int s = 0; s < pairs; ++s) {
       if (ahead == pairs) {  // at the end of the last pair but two
         tile = next;
         ahead = pairs - 1;
@@ -316,48 +348,68 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
           ahead = 0;
         }
       }
-      // the second half of this step's rows is read under the products of the
-      // first half
+      const bool behind = 2 * s + 1 == steps;  // the second step is behind the row
+      const int gs = 2 * s & 2;                // the pair's first step in its group
 #pragma unroll
-      for (int t = MH; t < MT; ++t)
-        read_a(buf, s & 1, t), sa[t] = scale(lds.as[grp], (hm * MT + t) * 16, s);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int e = 0; e < 2; ++e) {
+        const uint8_t* as = e && behind ? lds.none : lds.as[grp];
+        // first half: the rows of the second are read under it
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+        for (int c = 0; c < 8; ++c) {
+          const int u = c >> 2, i = c & 3;
 #pragma unroll
-        for (int j = 0; j < MH; ++j) acc[i][j] = mfma_mx4(fw[i], fa[j], acc[i][j], sw[i], sa[j]);
-        __builtin_amdgcn_sched_barrier(0);
+          for (int j = 0; j < JH; ++j)
+            acc[i][j] = mfma_mx4(fw[i][u], fa[j][u], acc[i][j], sw[i], sa[j], u);
+          if (c < JT) read_a(buf, e, JH + (c >> 1), c & 1);
+          if (c < JH) sa[JH + c] = scales(as, (hm * JT + JH + c) * 32 + r, gs + e);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (e) {
+          // this wave has read all of the pair, and its copies of the next
+          // have landed; after the barrier that holds for all waves
+          wait_barrier<0>();
+          buf ^= 1;
+          grp ^= s + 1 == pairs || gs ? 1 : 0;
+        }
+        const int ns = e ? (s + 1 == pairs ? 0 : (gs + 2) & 2) : gs + 1;  // the next step in its group
+        const uint8_t* nas = !e && behind ? lds.none : lds.as[grp];
+        const uint8_t* nws = !e && behind ? lds.none : lds.ws[grp];
+        // second half: the next step's operands are read under it, and the
+        // pair two ahead copied into the buffer just read
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const int u = c >> 2, i = c & 3;
+#pragma unroll
+          for (int j = JH; j < JT; ++j)
+            acc[i][j] = mfma_mx4(fw[i][u], fa[j][u], acc[i][j], sw[i], sa[j], u);
+          read_w(buf, 1 - e, i, u);
+          if (u) sw[i] = scales(nws, hn * 128 + i * 32 + rn, ns);
+          if (c < JT) read_a(buf, 1 - e, c >> 1, c & 1);
+          if (c < JH) sa[c] = scales(nas, (hm * JT + c) * 32 + r, ns);
+          if (e) {
+#pragma unroll
+            for (int d = c * kCopies / 8; d < (c + 1) * kCopies / 8; ++d) copy(ahead, d);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
-      const int step = s + 1 < steps ? s + 1 : 0;  // the next
-      if (!(step & 1)) {
-        // this wave has read all of the pair, and its copies of the next have
-        // landed; after the barrier that holds for all waves
-        wait_barrier<0>();
-        copy(ahead++);
-        buf ^= 1;
-        grp ^= step & 2 ? 0 : 1;
-      }
-      // the next step's operands, under the products of the second half
-#pragma unroll
-      for (int t = 0; t < MH; ++t)
-        read_a(buf, step & 1, t), sa[t] = scale(lds.as[grp], (hm * MT + t) * 16, step);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-#pragma unroll
-        for (int j = MH; j < MT; ++j) acc[i][j] = mfma_mx4(fw[i], fa[j], acc[i][j], sw[i], sa[j]);
-        read_w(buf, step & 1, i), sw[i] = scale(lds.ws[grp], hn * 128 + i * 16, step);
-        __builtin_amdgcn_sched_barrier(0);
-      }
+      ++ahead;
+      c_buf ^= 1;
     }
 #pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      const int m = tile.m0 + (hm * MT + j) * 16 + r;
+    for (int j = 0; j < JT; ++j) {
+      const int m = tile.m0 + (hm * JT + j) * 32 + r;
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const int nn = tile.n0 + hn * 128 + (i >> 1) * 32 + g * 8;
-        if (m < tile.hi)
-          store8_of<kBF16>(p.y, (size_t)m * p.n + nn, p.n - nn, acc[i][j], acc[i + 1][j]);
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int v = 0; v < 16; v += 8) {
+          const int nn = tile.n0 + hn * 128 + i * 32 + v * 2 + h * 8;
+          const f32x16& c = acc[i][j];
+          if (m < tile.hi)
+            store8_of<kBF16>(p.y, (size_t)m * p.n + nn, p.n - nn,
+                             f32x4{c[v], c[v + 1], c[v + 2], c[v + 3]},
+                             f32x4{c[v + 4], c[v + 5], c[v + 6], c[v + 7]});
+        }
       }
       __builtin_amdgcn_sched_barrier(0);  // one row of accumulators at a time: no spills
     }
@@ -425,16 +477,16 @@ hipError_t launch_expert_mx4(const mb_dims& d, const Geometry& g, const mb_plan_
   const int64_t rows = (int64_t)d.n_tokens * d.top_k;
   if (k_in >= 384 && rows >= (int64_t)d.n_ranks * g.NS * 128) {
     if (d.dtype_out == MB_BF16)
-      hipLaunchKernelGGL((k_expert_tile<true, 8>), dim3(kCus), dim3(kExpertThreads), 0, st, p);
+      hipLaunchKernelGGL((k_expert_tile<true, 4>), dim3(kCus), dim3(kExpertThreads), 0, st, p);
     else
-      hipLaunchKernelGGL((k_expert_tile<false, 8>), dim3(kCus), dim3(kExpertThreads), 0, st, p);
+      hipLaunchKernelGGL((k_expert_tile<false, 4>), dim3(kCus), dim3(kExpertThreads), 0, st, p);
     return hipGetLastError();
   }
   if (k_in >= 384 && rows >= (int64_t)d.n_ranks * g.NS * 32) {
     if (d.dtype_out == MB_BF16)
-      hipLaunchKernelGGL((k_expert_tile<true, 4>), dim3(kCus), dim3(kExpertThreads), 0, st, p);
+      hipLaunchKernelGGL((k_expert_tile<true, 2>), dim3(kCus), dim3(kExpertThreads), 0, st, p);
     else
-      hipLaunchKernelGGL((k_expert_tile<false, 4>), dim3(kCus), dim3(kExpertThreads), 0, st, p);
+      hipLaunchKernelGGL((k_expert_tile<false, 2>), dim3(kCus), dim3(kExpertThreads), 0, st, p);
     return hipGetLastError();
   }
   const int grid = 1024;
