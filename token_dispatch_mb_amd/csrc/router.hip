@@ -14,6 +14,7 @@ namespace mb {
 namespace {
 
 constexpr int kRouteWaves = 4;
+constexpr int kRouteGroups = 2048;  // workgroups of one launch: eight on each CU
 
 template <bool kBF16>
 __device__ __forceinline__ float load_logit(const void* p, size_t i) {
@@ -21,6 +22,24 @@ __device__ __forceinline__ float load_logit(const void* p, size_t i) {
     return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
   else
     return static_cast<const float*>(p)[i];
+}
+
+// V consecutive logits at i (a multiple of 4), `left` of them in the row.
+template <bool kBF16, int V>
+__device__ __forceinline__ void load_row(const void* p, size_t i, int left, float* v) {
+#pragma unroll
+  for (int j = 0; j < V; j += 4) {
+    if (j >= left) {
+      v[j] = v[j + 1] = v[j + 2] = v[j + 3] = -INFINITY;
+    } else if constexpr (kBF16) {
+      const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i + j);
+      v[j] = __uint_as_float(u.x << 16), v[j + 1] = __uint_as_float(u.x & 0xffff0000u);
+      v[j + 2] = __uint_as_float(u.y << 16), v[j + 3] = __uint_as_float(u.y & 0xffff0000u);
+    } else {
+      const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i + j);
+      v[j] = f.x, v[j + 1] = f.y, v[j + 2] = f.z, v[j + 3] = f.w;
+    }
+  }
 }
 
 // Logit or bias that masks its expert.
@@ -181,8 +200,336 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route(RouteArgs a) {
   route_exact<kBF16, V>(a, t, lane, arr[wave]);
 }
 
+// ---- four tokens to a wave, in binary32 --------------------------------------
+//
+// A token on a row of 16 lanes, V consecutive experts to a lane. Choice
+// values become integer keys whose low bits hold the expert's place in its
+// lane, so that sorting moves one register per expert; each lane sorts its
+// keys once, and a round takes the largest head of the row (four DPP steps)
+// and shifts the list of the lane that owned it. Everything is compared in
+// binary32, which decides unless two values come closer than its rounding.
+// Such neighbours among the first K + 1 are ranked by their binary64 values
+// (a lane computes one); a row where that does not settle it (the last open
+// and the first closed group, more candidates than K + 1, softmax scores with
+// a bias, masked or infinite choices) is done again by route_exact. bf16
+// logits compared as themselves have 16 free bits: their keys hold the whole
+// expert id and are exact, ties included.
+
+template <int kCtrl>
+__device__ __forceinline__ int dpp_i32(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, kCtrl, 0xf, 0xf, true);
+}
+
+// Float bits to integers of the same order, and back. (Sorting compares
+// integers: a float maximum of bits the compiler did not compute costs two
+// more instructions, in case they are a signalling NaN.)
+__device__ __forceinline__ int sortable(float f) {
+  const int b = __float_as_int(f);
+  return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float unsortable(int s) {
+  return __int_as_float(s ^ ((s >> 31) & 0x7fffffff));
+}
+
+__device__ __forceinline__ int row_max_i32(int v) {
+  v = max(v, dpp_i32<0xB1>(v));
+  v = max(v, dpp_i32<0x4E>(v));
+  v = max(v, dpp_i32<0x141>(v));
+  return max(v, dpp_i32<0x140>(v));
+}
+
+// By value: of two array elements the compiler would choose the index.
+__device__ __forceinline__ int choose(bool c, int a, int b) { return c ? a : b; }
+
+// a >= b
+__device__ __forceinline__ void order(int& a, int& b) {
+  const int t = max(a, b);
+  b = min(a, b);
+  a = t;
+}
+
+// N (a power of two) values at k, descending: odd-even merge sort.
+template <int N>
+__device__ __forceinline__ void sort_desc(int* k) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int d = p; d >= 1; d /= 2)
+#pragma unroll
+      for (int j = d % p; j + d < N; j += 2 * d)
+#pragma unroll
+        for (int i = 0; i < d; ++i)
+          if (i + j + d < N && (i + j) / (2 * p) == (i + j + d) / (2 * p)) order(k[i + j], k[i + j + d]);
+}
+
+// The 8 largest of two descending lists of 8, descending, into a.
+__device__ __forceinline__ void merge8(int* a, const int* b) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] = max(a[i], b[7 - i]);
+#pragma unroll
+  for (int d = 4; d >= 1; d /= 2)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!(i & d)) order(a[i], a[i + d]);
+}
+
+constexpr float kHuge = 3e38f;  // choice values past it are masks or infinities
+
+// Rows of 16 lanes counting how many of the other 15 hold more than v.
+template <int kRor>
+__device__ __forceinline__ int lanes_above(float v) {
+  if constexpr (kRor == 16) {
+    return 0;
+  } else {
+    const float o = __int_as_float(dpp_i32<0x120 + kRor>(__float_as_int(v)));
+    return (o > v ? 1 : 0) + lanes_above<kRor + 1>(v);
+  }
+}
+
+// Lanes of the row whose value comes before this one's: larger, or equal with
+// a lower id.
+template <int kRor>
+__device__ __forceinline__ int lanes_ahead(double v, int id) {
+  if constexpr (kRor == 16) {
+    return 0;
+  } else {
+    const int o_id = dpp_i32<0x120 + kRor>(id);
+    const double o = __hiloint2double(dpp_i32<0x120 + kRor>(__double2hiint(v)),
+                                      dpp_i32<0x120 + kRor>(__double2loint(v)));
+    return (o > v || (o == v && o_id < id) ? 1 : 0) + lanes_ahead<kRor + 1>(v, id);
+  }
+}
+
+template <bool kBF16, int V, bool kByLogit, bool kGrouped>
+__global__ __launch_bounds__(64 * kRouteWaves) void k_route_rows(RouteArgs a, int quads) {
+  constexpr int L = V < 8 ? V : 8;  // length of a lane's list
+  constexpr int VE = (V + 3) / 4;
+  constexpr bool kWholeId = kBF16 && kByLogit;
+  constexpr int kIdBits = V <= 1 ? 0 : V <= 2 ? 1 : V <= 4 ? 2 : V <= 8 ? 3 : V <= 16 ? 4 : 5;
+  constexpr int kIdMask = (1 << kIdBits) - 1;
+  constexpr float kLog2e = 1.44269504f;
+  __shared__ double arr[kGrouped ? kRouteWaves : 1][kGrouped ? VE * 64 : 1];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = lane & 15, row = lane >> 4;
+  const int e0 = q * V;
+  // How far rounding may move the difference of two choice values, relative to
+  // their magnitude and the largest bias: keys lose 2^-(23 - bits) twice,
+  // scores are off by 2^-22 each (softmax: by |l - max| 2^-23, and 0 below
+  // e^-87).
+  const float tol = kByLogit ? 0x1p-17f
+                    : !a.sigmoid ? 0x1p-15f
+                                 : (kIdBits <= 4 ? 0x1p-17f : 0x1p-16f);
+  const float tol_group = a.sigmoid ? 0x1p-20f : 0x1p-15f;  // no keys yet
+  constexpr float kTiny = 0x1p-100f;  // below it the places in the keys count
+  float b[V], bmax = 0.0f;
+  if constexpr (!kByLogit) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      b[i] = a.bias && e0 + i < a.E ? a.bias[e0 + i] : 0.0f;
+      if (masks(b[i])) b[i] = -INFINITY;
+      if (fabsf(b[i]) < INFINITY) bmax = fmaxf(bmax, fabsf(b[i]));
+    }
+    bmax = row_max_f32(bmax);
+  }
+  for (int w = blockIdx.x * kRouteWaves + wave; w < quads; w += gridDim.x * kRouteWaves) {
+    // rows past the last token repeat it and store nothing
+    const int t = min(w * 4 + row, a.N - 1);
+    const size_t at = (size_t)t * a.E;
+    float c[V];
+    if (V % 4 == 0 && (a.E & 3) == 0) {
+      load_row<kBF16, V>(a.logits, at + e0, a.E - e0, c);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] = e0 + i < a.E ? load_logit<kBF16>(a.logits, at + e0 + i) : -INFINITY;
+    }
+    float mx = -INFINITY, z = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = c[i] > -INFINITY ? c[i] : -INFINITY;  // NaN masks too
+    if (!a.sigmoid && (!kByLogit || !a.renorm)) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) mx = fmaxf(mx, c[i]);
+      mx = row_max_f32(mx);
+#pragma unroll
+      for (int i = 0; i < V; ++i) z += __builtin_amdgcn_exp2f((c[i] - mx) * kLog2e);
+      z = row_sum_f32(z);
+    }
+    if constexpr (!kByLogit) {
+      if (a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-c[i] * kLog2e));
+          c[i] = c[i] > -INFINITY ? s + b[i] : -INFINITY;
+        }
+      } else {
+        const float rz = 1.0f / z;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float s = __builtin_amdgcn_exp2f((c[i] - mx) * kLog2e) * rz;
+          c[i] = c[i] > -INFINITY ? s + b[i] : -INFINITY;
+        }
+      }
+    }
+    bool again = !(mx < INFINITY) || (!a.sigmoid && !(z < INFINITY));
+    int k[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i)  // + 0: one zero, whatever its sign
+      k[i] = sortable(__builtin_amdgcn_fmed3f(c[i] + 0.0f, -kHuge, kHuge));
+    bool open = true;
+    if constexpr (kGrouped) {
+      const int lanes = a.E / a.G / V;  // of a group: 1, 2, 4 or 8
+      int t1 = INT32_MIN, t2 = INT32_MIN;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        t2 = max(t2, min(t1, k[i]));
+        t1 = max(t1, k[i]);
+      }
+      auto join = [&](int o1, int o2) {
+        t2 = max(min(t1, o1), max(t2, o2));
+        t1 = max(t1, o1);
+      };
+      if (lanes > 1) join(dpp_i32<0xB1>(t1), dpp_i32<0xB1>(t2));
+      if (lanes > 2) join(dpp_i32<0x4E>(t1), dpp_i32<0x4E>(t2));
+      if (lanes > 4) join(dpp_i32<0x141>(t1), dpp_i32<0x141>(t2));
+      const float f1 = unsortable(t1), f2 = unsortable(t2);
+      // with a masked second best the sum is -inf
+      const float gs = a.group_top == 1 ? f1 : f2 > -kHuge ? f1 + f2 : -kHuge;
+      open = lanes_above<1>(gs) < a.top_groups * lanes;
+      const uint32_t seg = (uint32_t)(ballot64(open) >> (row * 16)) & 0xffffu;
+      const int gk = sortable(gs);
+      const float low = unsortable(~row_max_i32(open ? ~gk : INT32_MIN));
+      const float high = unsortable(row_max_i32(open ? INT32_MIN : gk));
+      // unless exactly top_groups groups are ahead of the rest by more than
+      // rounding, and their scores are numbers
+      again |= __popc(seg) != a.top_groups * lanes || !(fabsf(low) < 0.99f * kHuge) ||
+               !(low - high > (kByLogit ? 0.0f : tol_group * (fabsf(low) + 2 * bmax + kTiny)));
+    }
+    // the low bits: larger for the lower id
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if constexpr (kWholeId)
+        k[i] = (k[i] & ~0xffff) | (0xffff - (e0 + i));
+      else
+        k[i] = (k[i] & ~kIdMask) | (kIdMask - i);
+      if (!open || e0 + i >= a.E) k[i] = INT32_MIN;
+    }
+    if constexpr (V <= 8) {
+      sort_desc<V>(k);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; i += 8) sort_desc<8>(k + i);
+#pragma unroll
+      for (int i = 8; i < V; i += 8) merge8(k, k + i);
+    }
+    // round j: lane j notes the j-th largest key and the lane it came from
+    int mine = INT32_MIN, from = 0, taken = 0;
+    const int rounds = kWholeId ? a.K : a.K + 2;
+    for (int j = 0; j < rounds; ++j) {
+      const int m = row_max_i32(k[0]);
+      bool win = k[0] == m;
+      if constexpr (!kWholeId) {
+        const int lowest = __ffs((uint32_t)(ballot64(win) >> (row * 16)) & 0xffffu) - 1;
+        win = q == lowest;  // equal keys one at a time
+        if (q == j) from = lowest;
+      }
+      if (q == j) mine = m;
+      taken += win;
+#pragma unroll
+      for (int i = 0; i + 1 < L; ++i) k[i] = choose(win, k[i + 1], k[i]);
+      k[L - 1] = choose(win, INT32_MIN, k[L - 1]);
+    }
+    const float value = unsortable(mine);
+    again |= (V > L && taken >= L) || (q < a.K && !(fabsf(value) < 0.99f * kHuge));
+    int id = 0;
+    if constexpr (kWholeId) {
+      if (q < a.K) id = 0xffff - (mine & 0xffff);
+    } else {
+      if (q <= a.K && mine != INT32_MIN) id = from * V + kIdMask - (mine & kIdMask);
+      // Neighbours too close to tell apart, among the first K + 1: those are
+      // put in order by their exact values, unless more may belong with them.
+      // (NaN stands for no key at all: nothing is close to it.)
+      const float next = unsortable(dpp_i32<0x101>(mine));  // row_shl 1
+      const bool close = q <= a.K && value - next <= tol * (fabsf(value) + bmax + kTiny);
+      const uint32_t seg = (uint32_t)(ballot64(close) >> (row * 16)) & 0xffffu;
+      const bool near = (seg & ((1u << a.K) - 1u)) != 0;
+      again |= near && (((seg >> (a.K - 1)) & 3u) == 3u || (!kByLogit && !a.sigmoid));
+      if (ballot64(near && !again) != 0) {
+        double d = -INFINITY;
+        int key = q <= a.K ? id : a.E + q;
+        if (q <= a.K && value > -0.99f * kHuge) {
+          d = load_logit<kBF16>(a.logits, at + id);
+          if constexpr (!kByLogit) d = 1.0 / (1.0 + exp(-d)) + (a.bias ? (double)a.bias[id] : 0.0);
+        }
+        const int place = lanes_ahead<1>(d, key);
+        const int moved = __builtin_amdgcn_ds_permute((row * 16 + place) * 4, id);
+        if (q < a.K) id = moved;
+      }
+    }
+    const uint64_t redo = ballot64(again);
+    const bool ours = q < a.K && !((redo >> (row * 16)) & 0xffffu);
+    if (!ours) id = 0;
+    const float l = load_logit<kBF16>(a.logits, at + id);
+    float e, norm = 1.0f;
+    if (a.sigmoid) {
+      const float neg = fminf(l, 0.0f);
+      const float shift = a.renorm ? row_max_f32(ours ? neg : -INFINITY) : 0.0f;
+      e = expf(neg - shift) / (1.0f + expf(-fabsf(l)));
+    } else {
+      e = expf(l - (a.renorm ? row_max_f32(ours ? l : -INFINITY) : mx));
+      norm = z;
+    }
+    if (a.renorm) norm = row_sum_f32(ours ? e : 0.0f);
+    if (ours && w * 4 + row < a.N) {
+      a.ids[(size_t)t * a.K + q] = id;
+      a.w[(size_t)t * a.K + q] = e / norm * a.scale;
+    }
+    for (uint64_t left = redo; left;) {
+      const int r = __builtin_ctzll(left) >> 4;
+      left &= ~(0xffffull << (r * 16));
+      if (w * 4 + r < a.N) route_exact<kBF16, VE>(a, (size_t)w * 4 + r, lane, arr[kGrouped ? wave : 0]);
+    }
+  }
+}
+
+// Whether k_route_rows<V> takes these sizes: groups must be whole lanes.
+bool rows_fit(const RouteArgs& a, int V, bool grouped) {
+  if (a.K > 14) return false;
+  if (!grouped) return true;
+  const int size = a.E / a.G;
+  return a.E == 16 * V && size % V == 0;
+}
+
+template <bool kBF16, int V>
+bool launch_rows(const RouteArgs& a, hipStream_t st) {
+  const bool grouped = a.top_groups < a.G;
+  const bool by_logit = !a.bias && (!grouped || a.group_top == 1);
+  if (!rows_fit(a, V, grouped)) return false;
+  const int quads = (a.N + 3) / 4;
+  const dim3 grid(min((quads + kRouteWaves - 1) / kRouteWaves, kRouteGroups)), block(64 * kRouteWaves);
+  if (by_logit) {
+    if (grouped)
+      hipLaunchKernelGGL((k_route_rows<kBF16, V, true, true>), grid, block, 0, st, a, quads);
+    else
+      hipLaunchKernelGGL((k_route_rows<kBF16, V, true, false>), grid, block, 0, st, a, quads);
+  } else {
+    if (grouped)
+      hipLaunchKernelGGL((k_route_rows<kBF16, V, false, true>), grid, block, 0, st, a, quads);
+    else
+      hipLaunchKernelGGL((k_route_rows<kBF16, V, false, false>), grid, block, 0, st, a, quads);
+  }
+  return true;
+}
+
 template <bool kBF16>
 void launch_route_t(const RouteArgs& a, hipStream_t st) {
+  const int need = (a.E + 15) / 16;
+  const bool done = need <= 1    ? launch_rows<kBF16, 1>(a, st)
+                    : need <= 4  ? launch_rows<kBF16, 4>(a, st)
+                    : need <= 8  ? launch_rows<kBF16, 8>(a, st)
+                    : need <= 16 ? launch_rows<kBF16, 16>(a, st)
+                    : need <= 24 ? launch_rows<kBF16, 24>(a, st)
+                    : need <= 32 ? launch_rows<kBF16, 32>(a, st)
+                                 : false;
+  if (done) return;
   const dim3 grid((a.N + kRouteWaves - 1) / kRouteWaves), block(64 * kRouteWaves);
   const int v = (a.E + 63) / 64;
   if (v <= 1)
