@@ -24,14 +24,12 @@ __device__ __forceinline__ float load_logit(const void* p, size_t i) {
     return static_cast<const float*>(p)[i];
 }
 
-// V consecutive logits at i (a multiple of 4), `left` of them in the row.
+// V consecutive logits at i, both multiples of 4.
 template <bool kBF16, int V>
-__device__ __forceinline__ void load_row(const void* p, size_t i, int left, float* v) {
+__device__ __forceinline__ void load_row(const void* p, size_t i, float* v) {
 #pragma unroll
-  for (int j = 0; j < V; j += 4) {
-    if (j >= left) {
-      v[j] = v[j + 1] = v[j + 2] = v[j + 3] = -INFINITY;
-    } else if constexpr (kBF16) {
+  for (int j = 0; j + 3 < V; j += 4) {
+    if constexpr (kBF16) {
       const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i + j);
       v[j] = __uint_as_float(u.x << 16), v[j + 1] = __uint_as_float(u.x & 0xffff0000u);
       v[j + 2] = __uint_as_float(u.y << 16), v[j + 3] = __uint_as_float(u.y & 0xffff0000u);
@@ -45,16 +43,60 @@ __device__ __forceinline__ void load_row(const void* p, size_t i, int left, floa
 // Logit or bias that masks its expert.
 __device__ __forceinline__ bool masks(float v) { return !(v > -INFINITY); }
 
-__device__ __forceinline__ double wave_sum_f64(double v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
-  return v;
+template <int kCtrl>
+__device__ __forceinline__ int dpp_i32(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, kCtrl, 0xf, 0xf, true);
 }
 
-__device__ __forceinline__ float wave_max_f32(float v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v = fmaxf(v, __shfl_xor(v, m));
-  return v;
+// Float bits to integers of the same order, and back. (Sorting compares
+// integers: a float maximum of bits the compiler did not compute costs two
+// more instructions, in case they are a signalling NaN.)
+__device__ __forceinline__ int sortable(float f) {
+  const int b = __float_as_int(f);
+  return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float unsortable(int s) {
+  return __int_as_float(s ^ ((s >> 31) & 0x7fffffff));
+}
+
+__device__ __forceinline__ int row_max_i32(int v) {
+  v = max(v, dpp_i32<0xB1>(v));
+  v = max(v, dpp_i32<0x4E>(v));
+  v = max(v, dpp_i32<0x141>(v));
+  return max(v, dpp_i32<0x140>(v));
+}
+
+__device__ __forceinline__ float wave_max_f32(float v) { return unsortable(wave_max_i32(sortable(v))); }
+
+template <int kCtrl>
+__device__ __forceinline__ double dpp_f64(double v) {
+  return __hiloint2double(dpp_i32<kCtrl>(__double2hiint(v)), dpp_i32<kCtrl>(__double2loint(v)));
+}
+
+__device__ __forceinline__ double lane_f64(double v, int lane) {
+  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), lane),
+                          __builtin_amdgcn_readlane(__double2loint(v), lane));
+}
+
+__device__ __forceinline__ double wave_sum_f64(double v) {
+  v += dpp_f64<0xB1>(v);
+  v += dpp_f64<0x4E>(v);
+  v += dpp_f64<0x141>(v);
+  v += dpp_f64<0x140>(v);
+  return (lane_f64(v, 0) + lane_f64(v, 16)) + (lane_f64(v, 32) + lane_f64(v, 48));
+}
+
+// The largest value of the wave and, among its holders, the lowest id: three
+// integer reductions (high words, low words, ids).
+__device__ __forceinline__ int wave_argmax(double v, int id, double& best) {
+  v += 0.0;  // one zero, whatever its sign
+  const int h0 = __double2hiint(v), l0 = __double2loint(v), neg = h0 >> 31;
+  const int hi = h0 ^ (neg & 0x7fffffff), lo = (l0 ^ neg) ^ INT32_MIN;  // in order, as signed words
+  const int mh = wave_max_i32(hi);
+  const int ml = wave_max_i32(hi == mh ? lo : INT32_MIN);
+  const int mneg = mh >> 31;
+  best = __hiloint2double(mh ^ (mneg & 0x7fffffff), (ml ^ INT32_MIN) ^ mneg);
+  return wave_min_i32(hi == mh && lo == ml ? id : INT32_MAX);
 }
 
 struct RouteArgs {
@@ -144,6 +186,7 @@ __device__ void route_exact(const RouteArgs& a, size_t t, int lane, double* arr)
     __builtin_amdgcn_wave_barrier();
     double t1 = -INFINITY, t2 = -INFINITY;
     if (lane < a.G) {
+#pragma unroll 8
       for (int i = 0; i < size; ++i) {
         const double v = arr[lane * size + i];
         t2 = fmax(t2, fmin(t1, v));
@@ -156,7 +199,7 @@ __device__ void route_exact(const RouteArgs& a, size_t t, int lane, double* arr)
     if (a.group_top == 2) s = t2 > -INFINITY ? t1 + t2 : -INFINITY;
     int above = 0;  // groups ahead of this lane's
     for (int g = 0; g < a.G; ++g) {
-      const double o = __shfl(s, g);
+      const double o = lane_f64(s, g);
       above += o > s || (o == s && g < lane);
     }
     const uint64_t open = ballot64(lane < a.G && above < a.top_groups);
@@ -177,12 +220,7 @@ __device__ void route_exact(const RouteArgs& a, size_t t, int lane, double* arr)
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (c[i] > bc || (c[i] == bc && id[i] < bid)) bc = c[i], bid = id[i];
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-      const double oc = __shfl_xor(bc, m);
-      const int oid = __shfl_xor(bid, m);
-      if (oc > bc || (oc == bc && oid < bid)) bc = oc, bid = oid;
-    }
+    bid = wave_argmax(bc, bid, bc);
     if (lane == k) mine = bid, masked = !(bc > -INFINITY);
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -214,29 +252,6 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route(RouteArgs a) {
 // a bias, masked or infinite choices) is done again by route_exact. bf16
 // logits compared as themselves have 16 free bits: their keys hold the whole
 // expert id and are exact, ties included.
-
-template <int kCtrl>
-__device__ __forceinline__ int dpp_i32(int v) {
-  return __builtin_amdgcn_update_dpp(0, v, kCtrl, 0xf, 0xf, true);
-}
-
-// Float bits to integers of the same order, and back. (Sorting compares
-// integers: a float maximum of bits the compiler did not compute costs two
-// more instructions, in case they are a signalling NaN.)
-__device__ __forceinline__ int sortable(float f) {
-  const int b = __float_as_int(f);
-  return b ^ ((b >> 31) & 0x7fffffff);
-}
-__device__ __forceinline__ float unsortable(int s) {
-  return __int_as_float(s ^ ((s >> 31) & 0x7fffffff));
-}
-
-__device__ __forceinline__ int row_max_i32(int v) {
-  v = max(v, dpp_i32<0xB1>(v));
-  v = max(v, dpp_i32<0x4E>(v));
-  v = max(v, dpp_i32<0x141>(v));
-  return max(v, dpp_i32<0x140>(v));
-}
 
 // By value: of two array elements the compiler would choose the index.
 __device__ __forceinline__ int choose(bool c, int a, int b) { return c ? a : b; }
@@ -294,8 +309,7 @@ __device__ __forceinline__ int lanes_ahead(double v, int id) {
     return 0;
   } else {
     const int o_id = dpp_i32<0x120 + kRor>(id);
-    const double o = __hiloint2double(dpp_i32<0x120 + kRor>(__double2hiint(v)),
-                                      dpp_i32<0x120 + kRor>(__double2loint(v)));
+    const double o = dpp_f64<0x120 + kRor>(v);
     return (o > v || (o == v && o_id < id) ? 1 : 0) + lanes_ahead<kRor + 1>(v, id);
   }
 }
@@ -331,17 +345,25 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_rows(RouteArgs a, in
     }
     bmax = row_max_f32(bmax);
   }
-  for (int w = blockIdx.x * kRouteWaves + wave; w < quads; w += gridDim.x * kRouteWaves) {
-    // rows past the last token repeat it and store nothing
-    const int t = min(w * 4 + row, a.N - 1);
-    const size_t at = (size_t)t * a.E;
-    float c[V];
-    if (V % 4 == 0 && (a.E & 3) == 0) {
-      load_row<kBF16, V>(a.logits, at + e0, a.E - e0, c);
+  // Logits of quad w; rows past the last token repeat it (and store nothing).
+  // Those of the next quad are fetched while the rounds of one run.
+  float c[V];
+  const bool whole = V % 4 == 0 && a.E == 16 * V;
+  auto fetch = [&](int w) {
+    const size_t i = (size_t)min(w * 4 + row, a.N - 1) * a.E + e0;
+    if (whole) {
+      load_row<kBF16, V>(a.logits, i, c);
     } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) c[i] = e0 + i < a.E ? load_logit<kBF16>(a.logits, at + e0 + i) : -INFINITY;
+      for (int j = 0; j < V; ++j) c[j] = e0 + j < a.E ? load_logit<kBF16>(a.logits, i + j) : -INFINITY;
     }
+  };
+  int w = blockIdx.x * kRouteWaves + wave;
+  const int stride = gridDim.x * kRouteWaves;
+  if (w < quads) fetch(w);
+  for (; w < quads; w += stride) {
+    const int t = min(w * 4 + row, a.N - 1);
+    const size_t at = (size_t)t * a.E;
     float mx = -INFINITY, z = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) c[i] = c[i] > -INFINITY ? c[i] : -INFINITY;  // NaN masks too
@@ -412,6 +434,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_rows(RouteArgs a, in
         k[i] = (k[i] & ~kIdMask) | (kIdMask - i);
       if (!open || e0 + i >= a.E) k[i] = INT32_MIN;
     }
+    if (w + stride < quads) fetch(w + stride);
     if constexpr (V <= 8) {
       sort_desc<V>(k);
     } else {
