@@ -204,11 +204,11 @@ def _check(t, name: str, dtype=None, numel: int | None = None, nbytes: int | Non
     dtype or too few elements / bytes."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor (it is on {t.device})")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype} (it is {t.dtype})")
     if numel is not None and t.numel() < numel:
         raise ValueError(f"{name} holds {t.numel()} elements, {numel} needed")
@@ -230,11 +230,22 @@ def _dims_key(dims: "Dims") -> tuple:
     return tuple(getattr(dims, n) for n, _ in Dims._fields_)
 
 
+# handle of a device's current stream, without a Stream object for it (1.5 us
+# of a call); absent in builds of torch without GPU support
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream, *tensors) -> ctypes.c_void_p:
     """The stream's HIP handle (torch's current stream by default), after
     checking that the given tensors live on the stream's GPU (a pointer into
     another GPU's memory would fault in the kernel)."""
     if stream is None:
+        if _raw_stream is not None:
+            at = torch.cuda.current_device()
+            for t in tensors:
+                if t is not None and t.get_device() != at:
+                    raise ValueError(f"a tensor is on {t.device}, the stream on cuda:{at}")
+            return ctypes.c_void_p(_raw_stream(at))
         stream = torch.cuda.current_stream()
     dev = stream.device
     for t in tensors:
@@ -457,9 +468,28 @@ def _rows(t, name: str) -> tuple[int, int, int]:
     return t.shape[0], t.shape[1], F32 if t.dtype == torch.float32 else BF16
 
 
-def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
-    lo, hi = a.data_ptr(), b.data_ptr()
-    return lo < hi + _nbytes(b) and hi < lo + _nbytes(a)
+def _distinct(*ins, outs, in_place: bool) -> None:
+    """Outputs overlap neither each other nor an input; with `in_place` the
+    first output is one of the inputs itself (which is then written)."""
+    spans = []
+    for i, (name, t) in enumerate(outs):
+        if t is not None and not (i == 0 and in_place):
+            lo = t.data_ptr()
+            spans.append((lo, lo + t.numel() * t.element_size(), 1, name))
+    for name, t in ins:
+        if t is not None:
+            lo = t.data_ptr()
+            spans.append((lo, lo + t.numel() * t.element_size(), 0, name))
+    spans.sort()
+    end, out, last = 0, 0, ""
+    for lo, hi, is_out, name in spans:
+        if lo < end and hi > lo and (out or is_out):
+            raise ValueError(f"{last} and {name} overlap: outputs must not overlap each other or "
+                             "the inputs (residual_out may be x or residual themselves)")
+        if hi > end:
+            end, out, last = hi, is_out, name
+        else:
+            out |= is_out
 
 
 def rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float, q: torch.Tensor,
@@ -477,14 +507,11 @@ def rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float, q: torch.Tens
     for name, t in (("residual", residual), ("residual_out", residual_out), ("y", y)):
         if t is not None:
             _check(t, name, x.dtype, numel=n * h)
-    ins = [t for t in (x, residual, weight) if t is not None]
-    outs = [t for t in (residual_out, y, q, q_scale) if t is not None]
-    for i, o in enumerate(outs):
-        for t in ins + outs[:i]:
-            in_place = o is residual_out and t is not weight and o.data_ptr() == t.data_ptr()
-            if n * h and _overlap(o, t) and not in_place:
-                raise ValueError("outputs must not overlap each other or the inputs (residual_out "
-                                 "may be x or residual themselves)")
+    _distinct(
+        ("x", x), ("residual", residual), ("weight", weight),
+        outs=(("residual_out", residual_out), ("y", y), ("q", q), ("q_scale", q_scale)),
+        in_place=residual_out is not None
+        and residual_out.data_ptr() in (x.data_ptr(), residual.data_ptr() if residual is not None else 0))
     rc = _lib.mb_rmsnorm_fp8(n, h, code, eps, _ptr(x), _ptr(residual), _ptr(weight),
                              _ptr(residual_out), _ptr(y), _ptr(q), _ptr(q_scale),
                              _stream(stream, x, residual, weight, residual_out, y, q, q_scale))

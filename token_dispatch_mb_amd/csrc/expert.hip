@@ -103,6 +103,17 @@ __device__ __forceinline__ int slot_of(const int* first, int nslots, int t) {
   return __builtin_amdgcn_readfirstlane(lo);
 }
 
+__device__ __forceinline__ i32x4 load16(const uint8_t* p) {
+  return *static_cast<const i32x4*>(__builtin_assume_aligned(p, 16));
+}
+
+// The scales of four steps; rows of scales are whole words.
+__device__ __forceinline__ i32x4 scales16(const uint8_t* p) {
+  i32x4 v;
+  __builtin_memcpy(&v, __builtin_assume_aligned(p, 4), 16);
+  return v;
+}
+
 template <bool kBF16>
 __device__ __forceinline__ void store4(void* y, size_t at, f32x4 v) {
   if constexpr (kBF16) {
@@ -162,6 +173,7 @@ __device__ __forceinline__ void wait_barrier() {
 // outputs in 8 consecutive accumulators: 16-byte bf16 stores.
 constexpr int kTileN = 256;
 constexpr int kCus = 256, kXcds = 8;
+constexpr int kFewGroups = 2048;
 constexpr int kGroupM = 4;  // row tiles whose columns are walked together
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
@@ -186,10 +198,6 @@ __device__ __forceinline__ void copy16(i32x4 buf, lds_ptr to, uint32_t voff, uin
                ::"s"((uint32_t)(uintptr_t)to), "v"(voff), "s"(buf), "s"(soff)
                : "memory");
 }
-__device__ __forceinline__ i32x4 piece_at(const uint8_t* p) {
-  return *static_cast<const i32x4*>(__builtin_assume_aligned(p, 16));
-}
-
 struct Tile {
   int m0, hi, n0, e;
 };
@@ -307,10 +315,10 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
   const int ow = (hn * 128 + rn) * 128, oa = (hm * 32 * JT + r) * 128;
   const int piece = ((2 * h) ^ ((r >> 1) & 7)) << 4;  // of (step 0, h, 0)
   auto read_w = [&](int buf, int step, int t, int u) {
-    fw[t][u] = piece_at(lds.w[buf] + ow + (piece ^ (step * 64 + u * 16)) + t * 32 * 128);
+    fw[t][u] = load16(lds.w[buf] + ow + (piece ^ (step * 64 + u * 16)) + t * 32 * 128);
   };
   auto read_a = [&](int buf, int step, int t, int u) {
-    fa[t][u] = piece_at(lds.a[buf] + oa + (piece ^ (step * 64 + u * 16)) + t * 32 * 128);
+    fa[t][u] = load16(lds.a[buf] + oa + (piece ^ (step * 64 + u * 16)) + t * 32 * 128);
   };
   // the two scales of a step (0..3 of its group), all rows at s
   auto scales = [&](const uint8_t* s, int row, int step) {
@@ -418,50 +426,93 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
   wait_barrier<0>();
 }
 
-// 64 x 64 tiles, operands straight from memory: wave w holds 16 outputs of
-// all 64 rows. Workgroups stride over the tiles.
-template <bool kBF16>
-__global__ __launch_bounds__(kExpertThreads) void k_expert_mx4(ExpertArgs p) {
+// ---- few rows to an expert: operands straight from memory --------------------
+//
+// The weights are read once each, and set the pace. A wave computes 16
+// outputs of 16 RT rows; a workgroup's four waves take 64 consecutive outputs
+// and share the rows through the caches. Four steps' weights (64 bytes of a
+// row a step) and the 16 bytes of their scales are fetched together.
+template <bool kBF16, int RT>
+__global__ __launch_bounds__(kExpertThreads) void k_expert_few(ExpertArgs p) {
   __shared__ int first[kMaxPlanSlots + 1];
   __shared__ int part[kExpertThreads / 64];
   if (p.status[0] & MB_ST_FATAL) return;
   const int nslots = p.P * p.NS;
-  tile_table<64>(p, nslots, first, part);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  tile_table<16 * RT>(p, nslots, first, part);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int ntn = (p.n + 63) / 64;
-  const int total = first[nslots];
-  const size_t kb = p.k / 2, ks = p.k / 32;
-  for (int64_t t = blockIdx.x; t < (int64_t)total * ntn; t += gridDim.x) {
+  const int64_t total = (int64_t)first[nslots] * ntn;
+  const int kb = p.k / 2, ks = p.k / 32, steps = p.k / 128;
+  for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
     const int mt = (int)(t / ntn), nt = (int)(t - (int64_t)mt * ntn);
     const int j = slot_of(first, nslots, mt);
     int lo, hi, e;
     slot_rows(p, j, lo, hi, e);
-    const int m0 = lo + (mt - first[j]) * 64;
+    const int m0 = lo + (mt - first[j]) * 16 * RT;
     const int n0 = nt * 64 + wave * 16;
     if (n0 >= p.n) continue;
     // rows past the slot's or the weights' end read the last one instead
     const size_t wr = (size_t)e * p.n + min(n0 + r, p.n - 1);
-    size_t ar[4];
+    const uint8_t* w = p.w + wr * kb + g * 16;
+    const uint8_t* ws = p.w_scale + wr * ks;
+    const uint8_t *a[RT], *as[RT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) ar[i] = min(m0 + i * 16 + r, hi - 1);
-    f32x4 acc[4] = {};
-    for (int kk = 0; kk < p.k / 128; ++kk) {
-      const i32x4 wv = *reinterpret_cast<const i32x4*>(p.w + wr * kb + kk * 64 + g * 16);
-      const int ws = p.w_scale[wr * ks + kk * 4 + g];
+    for (int i = 0; i < RT; ++i) {
+      const size_t ar = min(m0 + i * 16 + r, hi - 1);
+      a[i] = p.a + ar * kb + g * 16;
+      as[i] = p.a_scale + ar * ks;
+    }
+    f32x4 acc[RT] = {};
+    int s = 0;
+    for (; s + 4 <= steps; s += 4) {
+      i32x4 wv[4], av[RT][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const i32x4 av = *reinterpret_cast<const i32x4*>(p.a + ar[i] * kb + kk * 64 + g * 16);
-        const int as = p.a_scale[ar[i] * ks + kk * 4 + g];
-        acc[i] = mfma_mx4(wv, av, acc[i], ws, as);
+      for (int u = 0; u < 4; ++u) wv[u] = load16(w + (s + u) * 64);
+      const i32x4 wd = scales16(ws + s * 4);
+      i32x4 ad[RT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) av[i][u] = load16(a[i] + (s + u) * 64);
+        ad[i] = scales16(as[i] + s * 4);
       }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+          acc[i] = mfma_mx4(wv[u], av[i][u], acc[i], (uint32_t)wd[u] >> (8 * g),
+                            (uint32_t)ad[i][u] >> (8 * g));
+    }
+    for (; s < steps; ++s) {
+      const i32x4 wv = load16(w + s * 64);
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+        acc[i] = mfma_mx4(wv, load16(a[i] + s * 64), acc[i], ws[s * 4 + g], as[i][s * 4 + g]);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RT; ++i) {
       const int m = m0 + i * 16 + r, nn = n0 + 4 * g;
       if (m < hi && nn < p.n) store4<kBF16>(p.y, (size_t)m * p.n + nn, acc[i]);
     }
   }
+}
+
+template <bool kBF16>
+void launch_expert_t(const ExpertArgs& p, int64_t rows, hipStream_t st) {
+  // rows to expect in a slot
+  const int64_t slots = (int64_t)p.P * p.NS;
+  const dim3 block(kExpertThreads);
+  if (p.k >= 384 && rows >= slots * 128)
+    hipLaunchKernelGGL((k_expert_tile<kBF16, 4>), dim3(kCus), block, 0, st, p);
+  else if (p.k >= 384 && rows >= slots * 32)
+    hipLaunchKernelGGL((k_expert_tile<kBF16, 2>), dim3(kCus), block, 0, st, p);
+  else if (rows >= slots * 16)
+    hipLaunchKernelGGL((k_expert_few<kBF16, 4>), dim3(kFewGroups), block, 0, st, p);
+  else if (rows >= slots * 8)
+    hipLaunchKernelGGL((k_expert_few<kBF16, 2>), dim3(kFewGroups), block, 0, st, p);
+  else
+    hipLaunchKernelGGL((k_expert_few<kBF16, 1>), dim3(kFewGroups), block, 0, st, p);
 }
 
 }  // namespace
@@ -475,25 +526,10 @@ hipError_t launch_expert_mx4(const mb_dims& d, const Geometry& g, const mb_plan_
                         o.cu_seqlens, o.rep_expert, o.status, d.n_ranks, d.n_experts,
                         g.Eh,      g.NS,    d.slots_per_rank, d.cap, n_out, k_in};
   const int64_t rows = (int64_t)d.n_tokens * d.top_k;
-  if (k_in >= 384 && rows >= (int64_t)d.n_ranks * g.NS * 128) {
-    if (d.dtype_out == MB_BF16)
-      hipLaunchKernelGGL((k_expert_tile<true, 4>), dim3(kCus), dim3(kExpertThreads), 0, st, p);
-    else
-      hipLaunchKernelGGL((k_expert_tile<false, 4>), dim3(kCus), dim3(kExpertThreads), 0, st, p);
-    return hipGetLastError();
-  }
-  if (k_in >= 384 && rows >= (int64_t)d.n_ranks * g.NS * 32) {
-    if (d.dtype_out == MB_BF16)
-      hipLaunchKernelGGL((k_expert_tile<true, 2>), dim3(kCus), dim3(kExpertThreads), 0, st, p);
-    else
-      hipLaunchKernelGGL((k_expert_tile<false, 2>), dim3(kCus), dim3(kExpertThreads), 0, st, p);
-    return hipGetLastError();
-  }
-  const int grid = 1024;
   if (d.dtype_out == MB_BF16)
-    hipLaunchKernelGGL(k_expert_mx4<true>, dim3(grid), dim3(kExpertThreads), 0, st, p);
+    launch_expert_t<true>(p, rows, st);
   else
-    hipLaunchKernelGGL(k_expert_mx4<false>, dim3(grid), dim3(kExpertThreads), 0, st, p);
+    launch_expert_t<false>(p, rows, st);
   return hipGetLastError();
 }
 

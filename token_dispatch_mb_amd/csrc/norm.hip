@@ -9,7 +9,7 @@
 namespace mb {
 namespace {
 
-constexpr int kNormThreads = 256;
+constexpr int kNormThreads = 512;
 constexpr float kE4m3Max = 448.0f;
 
 // One workgroup per row, a lane per 8 consecutive elements, the row in
@@ -52,16 +52,17 @@ __global__ __launch_bounds__(kNormThreads) void k_rmsnorm_fp8(
   for (int i = 0; i < CPT; ++i) {
     const int c = i * kNormThreads + threadIdx.x;
     if (c < chunks) {
-      float g[8], v[8], amax = 0.0f;
+      float g[8], v[8];
+      uint32_t bits = 0;
       load8<kBF16>(weight, c, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        v[j] = bad ? NAN : h[i][j] * inv * g[j];
-        amax = fmaxf(amax, fabsf(v[j]));
+        v[j] = h[i][j] * inv * g[j];
+        bits = max(bits, __float_as_uint(v[j]) & 0x7fffffffu);
       }
-      if (y) store8<kBF16>(y, row + c, v);
+      if (y) store8<kBF16>(y, row + c, v);  // all NaN when bad: inv is
       // 16 lanes of 8 elements share a block
-      amax = row_max_f32(amax);
+      const float amax = __uint_as_float(row_max_u32(bits));
       const bool tiny = amax < 0x1p-110f;
       const float scale = tiny ? 1.0f : amax * (1.0f / kE4m3Max);
       const float f = tiny ? 0.0f : kE4m3Max / amax;

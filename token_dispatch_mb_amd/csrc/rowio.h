@@ -36,16 +36,21 @@ __device__ __forceinline__ void load8(const void* p, size_t c, float* v) {
   }
 }
 
+// Nontemporal: rows leave for memory (8192 x 7168 bf16 rows read back from
+// 4 bits: 46 us with the quantisation before it, 51 with plain stores; the
+// norm of 131072 such rows 2 % faster).
 template <bool kBF16>
 __device__ __forceinline__ void store8(void* p, size_t c, const float* v) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
   if constexpr (kBF16) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = bf16x2_rne(v[2 * i], v[2 * i + 1]);
-    static_cast<uint4*>(p)[c] = uint4{w[0], w[1], w[2], w[3]};
+    __builtin_nontemporal_store(u32x4{w[0], w[1], w[2], w[3]}, static_cast<u32x4*>(p) + c);
   } else {
-    static_cast<float4*>(p)[2 * c] = float4{v[0], v[1], v[2], v[3]};
-    static_cast<float4*>(p)[2 * c + 1] = float4{v[4], v[5], v[6], v[7]};
+    __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, static_cast<f32x4*>(p) + 2 * c);
+    __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, static_cast<f32x4*>(p) + 2 * c + 1);
   }
 }
 

@@ -110,15 +110,29 @@ __device__ __forceinline__ float dpp_f32(float v) {
       __builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, 0xf, 0xf, true));
 }
 
-__device__ __forceinline__ float quad_max_f32(float v) {
-  v = fmaxf(v, dpp_f32<0xB1>(v));
-  return fmaxf(v, dpp_f32<0x4E>(v));
-}
-
 __device__ __forceinline__ float row_max_f32(float v) {
-  v = quad_max_f32(v);
+  v = fmaxf(v, dpp_f32<0xB1>(v));
+  v = fmaxf(v, dpp_f32<0x4E>(v));
   v = fmaxf(v, dpp_f32<0x141>(v));
   return fmaxf(v, dpp_f32<0x140>(v));
+}
+
+// Maxima of magnitudes go by their bits: positive floats are in the order of
+// their bits, with infinity and NaN at the top.
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xf, 0xf, true);
+}
+
+__device__ __forceinline__ uint32_t quad_max_u32(uint32_t v) {
+  v = max(v, dpp_u32<0xB1>(v));
+  return max(v, dpp_u32<0x4E>(v));
+}
+
+__device__ __forceinline__ uint32_t row_max_u32(uint32_t v) {
+  v = quad_max_u32(v);
+  v = max(v, dpp_u32<0x141>(v));
+  return max(v, dpp_u32<0x140>(v));
 }
 
 __device__ __forceinline__ float row_sum_f32(float v) {
