@@ -124,6 +124,11 @@ __device__ __forceinline__ void store4(void* y, size_t at, f32x4 v) {
   }
 }
 
+// Waits until this wave's LDS reads are done, then for the other waves.
+__device__ __forceinline__ void read_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 // Outputs [at, at + 8) of a row, as many as are left (a multiple of 4).
 template <bool kBF16>
 __device__ __forceinline__ void store8_of(void* y, size_t at, int left, f32x4 v, f32x4 u) {
@@ -159,8 +164,10 @@ __device__ __forceinline__ void wait_barrier() {
 // cache line. (With single steps, 64 bytes of a row and 4 of its scales at a
 // time, the L2's requests set the pace.) The scales are copied in groups of
 // four steps, 16 bytes of every row. Two pairs and two groups are in LDS; the
-// pair two ahead is copied as soon as the last operand of the present one is
-// in registers. The pairs of a workgroup's tiles form one sequence, so that a
+// pair two ahead is copied over the present one, its weights once all of
+// these are in registers, the rest half a step later. (All copies in that
+// last half step held up the products: the address unit takes 16 cycles for
+// each of 72.) The pairs of a workgroup's tiles form one sequence, so that a
 // tile's first copies run under the end of the tile before it.
 //
 // LDS layout of a pair: rows of 128 bytes, the 16-byte piece c of a row at
@@ -370,12 +377,14 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
             acc[i][j] = mfma_mx4(fw[i][u], fa[j][u], acc[i][j], sw[i], sa[j], u);
           if (c < JT) read_a(buf, e, JH + (c >> 1), c & 1);
           if (c < JH) sa[JH + c] = scales(as, (hm * JT + JH + c) * 32 + r, gs + e);
+          if (e) copy(ahead, c);
           __builtin_amdgcn_sched_barrier(0);
         }
         if (e) {
           // this wave has read all of the pair, and its copies of the next
-          // have landed; after the barrier that holds for all waves
-          wait_barrier<0>();
+          // have landed (the eight just issued are of the one after); after
+          // the barrier that holds for all waves
+          wait_barrier<8>();
           buf ^= 1;
           grp ^= s + 1 == pairs || gs ? 1 : 0;
         }
@@ -396,10 +405,12 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
           if (c < JH) sa[c] = scales(nas, (hm * JT + c) * 32 + r, ns);
           if (e) {
 #pragma unroll
-            for (int d = c * kCopies / 8; d < (c + 1) * kCopies / 8; ++d) copy(ahead, d);
+            for (int d = 8 + c * (kCopies - 8) / 8; d < 8 + (c + 1) * (kCopies - 8) / 8; ++d)
+              copy(ahead, d);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
+        if (!e) read_barrier();  // all weights of the pair are in registers
       }
       ++ahead;
       c_buf ^= 1;
