@@ -165,9 +165,10 @@ __device__ __forceinline__ void wait_barrier() {
 // time, the L2's requests set the pace.) The scales are copied in groups of
 // four steps, 16 bytes of every row. Two pairs and two groups are in LDS; the
 // pair two ahead is copied over the present one, its weights once all of
-// these are in registers, the rest half a step later. (All copies in that
-// last half step held up the products: the address unit takes 16 cycles for
-// each of 72.) The pairs of a workgroup's tiles form one sequence, so that a
+// these are in registers, its rows half a step later, its scales under the
+// next pair's first half step. (All copies in one half step held up the
+// products: the address unit takes 16 cycles for each of 64, and 64 for each
+// of the scales' eight, which fetch from 64 lines.) The pairs of a workgroup's tiles form one sequence, so that a
 // tile's first copies run under the end of the tile before it.
 //
 // LDS layout of a pair: rows of 128 bytes, the 16-byte piece c of a row at
@@ -284,31 +285,34 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
     ra = buffer_of(p.a + (size_t)next.m0 * kb, (uint32_t)na * kb);
     ras = buffer_of(p.a_scale + (size_t)next.m0 * ks, (uint32_t)na * ks);
   };
-  // Copy c of the kCopies of a pair. With an odd number of steps the second
-  // half of the last pair lies behind the row: its lanes read out of range,
-  // zeros.
-  constexpr int kCopies = 8 + 2 * JT + 2;
-  auto copy = [&](int pair, int c) {
+  // Copy c of a pair's rows: 8 of weights, then 2 JT. With an odd number of
+  // steps the second half of the last pair lies behind the row: its lanes
+  // read out of range, zeros.
+  auto copy_w = [&](int pair, int c) {
     const uint32_t last = 2 * pair + 1 == steps ? 0x80000000u : 0u;
-    if (c < 8) {
-      copy16(rw, (lds_ptr)(lds.w[c_buf] + (wave * 8 + c) * 1024),
-             (cw[c & 1] + (wave * 8 + c) * 8 * kb) | (cut_w & last), pair * 128);
-    } else if (c < 8 + 2 * JT) {
-      const int j = c - 8;
-      copy16(ra, (lds_ptr)(lds.a[c_buf] + (wave * 2 * JT + j) * 1024),
-             (ca[j & 1] + (wave * 2 * JT + j) * 8 * kb) | (cut_a[j & 1] & last), pair * 128);
+    copy16(rw, (lds_ptr)(lds.w[c_buf] + (wave * 8 + c) * 1024),
+           (cw[c & 1] + (wave * 8 + c) * 8 * kb) | (cut_w & last), pair * 128);
+  };
+  auto copy_a = [&](int pair, int c) {
+    const uint32_t last = 2 * pair + 1 == steps ? 0x80000000u : 0u;
+    copy16(ra, (lds_ptr)(lds.a[c_buf] + (wave * 2 * JT + c) * 1024),
+           (ca[c & 1] + (wave * 2 * JT + c) * 8 * kb) | (cut_a[c & 1] & last), pair * 128);
+  };
+  // The scales of a pair and the next; nothing in the second pair of a group.
+  // They follow half a pair after the rows, by when the rows' descriptors may
+  // be those of the next tile.
+  i32x4 late_ws, late_as;
+  int late_pair = 0;
+  auto copy_scales = [&](int c) {
+    const bool group = !(late_pair & 1);
+    const uint32_t none = group ? 0u : 0x80000000u;
+    if (c == 0) {
+      c_group ^= group ? 1 : 0;
+      copy16(late_ws, (lds_ptr)((group ? lds.ws[c_group] : lds.none) + wave * 1024), csw | none,
+             (late_pair >> 1) * 16);
     } else {
-      // the scales of this pair and the next; nothing in the second of a group
-      const bool group = !(pair & 1);
-      const uint32_t none = group ? 0u : 0x80000000u;
-      if (c == 8 + 2 * JT) {
-        c_group ^= group ? 1 : 0;
-        copy16(rws, (lds_ptr)((group ? lds.ws[c_group] : lds.none) + wave * 1024), csw | none,
-               (pair >> 1) * 16);
-      } else {
-        copy16(ras, (lds_ptr)((group ? lds.as[c_group] : lds.none) + wave * 1024), csa | none,
-               (pair >> 1) * 16);
-      }
+      copy16(late_as, (lds_ptr)((group ? lds.as[c_group] : lds.none) + wave * 1024), csa | none,
+             (late_pair >> 1) * 16);
     }
   };
 
@@ -334,11 +338,17 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
 
   aim(0);
 #pragma unroll
-  for (int c = 0; c < kCopies; ++c) copy(0, c);
-  c_buf = 1;
+  for (int pair = 0; pair < 2; ++pair) {
 #pragma unroll
-  for (int c = 0; c < kCopies; ++c) copy(1, c);
-  c_buf = 0;
+    for (int c = 0; c < 8; ++c) copy_w(pair, c);
+#pragma unroll
+    for (int c = 0; c < 2 * JT; ++c) copy_a(pair, c);
+    c_buf ^= 1;
+  }
+  late_ws = rws, late_as = ras;
+  copy_scales(0);
+  copy_scales(1);
+  late_pair = 1;
   wait_barrier<0>();
   int buf = 0, grp = 0, ahead = 2;
 #pragma unroll
@@ -377,7 +387,8 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
             acc[i][j] = mfma_mx4(fw[i][u], fa[j][u], acc[i][j], sw[i], sa[j], u);
           if (c < JT) read_a(buf, e, JH + (c >> 1), c & 1);
           if (c < JH) sa[JH + c] = scales(as, (hm * JT + JH + c) * 32 + r, gs + e);
-          if (e) copy(ahead, c);
+          if (e) copy_w(ahead, c);
+          if (!e && c < 2) copy_scales(c);
           __builtin_amdgcn_sched_barrier(0);
         }
         if (e) {
@@ -405,14 +416,14 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
           if (c < JH) sa[c] = scales(nas, (hm * JT + c) * 32 + r, ns);
           if (e) {
 #pragma unroll
-            for (int d = 8 + c * (kCopies - 8) / 8; d < 8 + (c + 1) * (kCopies - 8) / 8; ++d)
-              copy(ahead, d);
+            for (int d = c * JT / 4; d < (c + 1) * JT / 4; ++d) copy_a(ahead, d);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
         if (!e) read_barrier();  // all weights of the pair are in registers
       }
-      ++ahead;
+      late_ws = rws, late_as = ras;
+      late_pair = ahead++;
       c_buf ^= 1;
     }
 #pragma unroll
