@@ -255,6 +255,17 @@ def test_norm_refuses_overlaps():
         mb.rmsnorm_fp8(x, w, 1e-6, q, qs, y=x)
     with pytest.raises(ValueError, match="overlap"):
         mb.rmsnorm_fp8(x[:3], w, 1e-6, q, qs, residual=x[:3], residual_out=x[1:])
+    with pytest.raises(ValueError, match="overlap"):
+        mb.rmsnorm_fp8(x, w, 1e-6, q, qs, residual=x.clone(), residual_out=x, y=x)
+    with pytest.raises(ValueError, match="overlap"):
+        mb.rmsnorm_fp8(x, w, 1e-6, x.view(torch.uint8), qs)
+    with pytest.raises(ValueError, match="overlap"):
+        mb.rmsnorm_fp8(x, x[1], 1e-6, q, qs, residual=x.clone(), residual_out=x)
+    with pytest.raises(ValueError, match="overlap"):
+        mb.rmsnorm_fp8(x, w, 1e-6, q, q.view(torch.float32))
+    one = x.clone()  # x as its own residual, in place: doubled
+    mb.rmsnorm_fp8(one, w, 1e-6, q, qs, residual=one, residual_out=one)
+    assert torch.equal(one, 2 * x)
     with pytest.raises(ValueError, match="two dimensions"):
         mb.rmsnorm_fp8(x[0], w, 1e-6, q, qs)
     with pytest.raises(TypeError, match="weight must be"):

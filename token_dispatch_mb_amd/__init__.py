@@ -195,7 +195,7 @@ def workspace_bytes(dims: Dims) -> int:
 
 
 def _ptr(t: torch.Tensor | None):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _check(t, name: str, dtype=None, numel: int | None = None, nbytes: int | None = None) -> None:
@@ -468,28 +468,19 @@ def _rows(t, name: str) -> tuple[int, int, int]:
     return t.shape[0], t.shape[1], F32 if t.dtype == torch.float32 else BF16
 
 
-def _distinct(*ins, outs, in_place: bool) -> None:
-    """Outputs overlap neither each other nor an input; with `in_place` the
-    first output is one of the inputs itself (which is then written)."""
-    spans = []
-    for i, (name, t) in enumerate(outs):
-        if t is not None and not (i == 0 and in_place):
-            lo = t.data_ptr()
-            spans.append((lo, lo + t.numel() * t.element_size(), 1, name))
-    for name, t in ins:
-        if t is not None:
-            lo = t.data_ptr()
-            spans.append((lo, lo + t.numel() * t.element_size(), 0, name))
+def _distinct(spans: list) -> None:
+    """Refuse outputs that overlap each other or an input: `spans` lists
+    (first byte, past the last, is it written)."""
     spans.sort()
-    end, out, last = 0, 0, ""
-    for lo, hi, is_out, name in spans:
-        if lo < end and hi > lo and (out or is_out):
-            raise ValueError(f"{last} and {name} overlap: outputs must not overlap each other or "
-                             "the inputs (residual_out may be x or residual themselves)")
+    end, written = 0, False
+    for lo, hi, out in spans:
+        if lo < end and hi > lo and (written or out):
+            raise ValueError("outputs must not overlap each other or the inputs (residual_out may "
+                             "be x or residual themselves)")
         if hi > end:
-            end, out, last = hi, is_out, name
+            end, written = hi, out
         else:
-            out |= is_out
+            written |= out
 
 
 def rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float, q: torch.Tensor,
@@ -501,19 +492,36 @@ def rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float, q: torch.Tens
     ``dispatch`` takes; optionally the sum x + residual (``residual_out``,
     which may be x or residual themselves) and the normed rows ``y``."""
     n, h, code = _rows(x, "x")
-    _check(weight, "weight", x.dtype, numel=h)
-    _check(q, "q", torch.uint8, numel=n * h)
+    dtype, m = x.dtype, n * h
+    _check(weight, "weight", dtype, numel=h)
+    _check(q, "q", torch.uint8, numel=m)
     _check(q_scale, "q_scale", torch.float32, numel=n * (h // 128))
-    for name, t in (("residual", residual), ("residual_out", residual_out), ("y", y)):
-        if t is not None:
-            _check(t, name, x.dtype, numel=n * h)
-    _distinct(
-        ("x", x), ("residual", residual), ("weight", weight),
-        outs=(("residual_out", residual_out), ("y", y), ("q", q), ("q_scale", q_scale)),
-        in_place=residual_out is not None
-        and residual_out.data_ptr() in (x.data_ptr(), residual.data_ptr() if residual is not None else 0))
-    rc = _lib.mb_rmsnorm_fp8(n, h, code, eps, _ptr(x), _ptr(residual), _ptr(weight),
-                             _ptr(residual_out), _ptr(y), _ptr(q), _ptr(q_scale),
+    ptr = x.data_ptr()
+    size = m * ELT_BYTES[code]
+    spans = [(ptr, ptr + size, False)]
+    p_r = p_o = p_y = None
+    if residual is not None:
+        _check(residual, "residual", dtype, numel=m)
+        p_r = residual.data_ptr()
+        spans.append((p_r, p_r + size, False))
+    if residual_out is not None:
+        _check(residual_out, "residual_out", dtype, numel=m)
+        p_o = residual_out.data_ptr()
+        if p_o == ptr or p_o == p_r:  # in place: that input is written
+            spans = [(lo, hi, lo == p_o) for lo, hi, _ in spans if lo != p_o or ptr != p_r]
+            if ptr == p_r:  # x and residual are one tensor
+                spans.append((ptr, ptr + size, True))
+        else:
+            spans.append((p_o, p_o + size, True))
+    if y is not None:
+        _check(y, "y", dtype, numel=m)
+        p_y = y.data_ptr()
+        spans.append((p_y, p_y + size, True))
+    p_w, p_q, p_s = weight.data_ptr(), q.data_ptr(), q_scale.data_ptr()
+    spans += [(p_w, p_w + size // n if n else p_w, False), (p_q, p_q + m, True),
+              (p_s, p_s + m // 32, True)]
+    _distinct(spans)
+    rc = _lib.mb_rmsnorm_fp8(n, h, code, eps, ptr, p_r, p_w, p_o, p_y, p_q, p_s,
                              _stream(stream, x, residual, weight, residual_out, y, q, q_scale))
     if rc != OK:
         raise MoebalError("mb_rmsnorm_fp8", rc)
