@@ -467,7 +467,7 @@ int mb_rmsnorm_fp8(int32_t n_rows, int32_t hidden, int32_t dtype, float eps, con
  *              2*hidden elements and v = gate / (1 + exp(-gate)) * up in fp32.
  *  x_dev       [n_rows, hidden or 2*hidden] of dtype (MB_F32, MB_BF16).
  *  row_src_dev [n_rows] int32 or NULL: rows with a negative entry (the
- *              padding rows of a plan's row_src) are neither read nor written.
+ *              padding rows of a plan's row_src) are not written.
  *  q_dev       [n_rows, hidden/2], q_scale_dev [n_rows, hidden/32].
  * hidden % 32 == 0, n_rows >= 0 and n_rows * ceil(hidden / 512) <= 2^26 - 16;
  * x and q 16-byte aligned, row_src 4-byte.

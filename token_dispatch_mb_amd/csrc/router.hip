@@ -353,6 +353,12 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_rows(RouteArgs a, in
     const size_t i = (size_t)min(w * 4 + row, a.N - 1) * a.E + e0;
     if (whole) {
       load_row<kBF16, V>(a.logits, i, c);
+    } else if (V % 4 == 0 && (a.E & 3) == 0) {
+#pragma unroll
+      for (int j = 0; j < V; j += 4) {
+        c[j] = c[j + 1] = c[j + 2] = c[j + 3] = -INFINITY;
+        if (e0 + j < a.E) load_row<kBF16, 4>(a.logits, i + j, c + j);
+      }
     } else {
 #pragma unroll
       for (int j = 0; j < V; ++j) c[j] = e0 + j < a.E ? load_logit<kBF16>(a.logits, i + j) : -INFINITY;
