@@ -7,6 +7,8 @@
 // that are a maximum), the logits themselves are compared.
 #include <math.h>
 
+#include <type_traits>
+
 #include "mb_internal.h"
 #include "wave.h"
 
@@ -290,14 +292,14 @@ __device__ __forceinline__ void merge8(int* a, const int* b) {
 
 constexpr float kHuge = 3e38f;  // choice values past it are masks or infinities
 
-// Rows of 16 lanes counting how many of the other 15 hold more than v.
-template <int kRor>
-__device__ __forceinline__ int lanes_above(float v) {
+// Groups of kLanes lanes of a row whose value is above this one's.
+template <int kLanes, int kRor = kLanes>
+__device__ __forceinline__ int groups_above(float v) {
   if constexpr (kRor == 16) {
     return 0;
   } else {
     const float o = __int_as_float(dpp_i32<0x120 + kRor>(__float_as_int(v)));
-    return (o > v ? 1 : 0) + lanes_above<kRor + 1>(v);
+    return (o > v ? 1 : 0) + groups_above<kLanes, kRor + kLanes>(v);
   }
 }
 
@@ -314,8 +316,10 @@ __device__ __forceinline__ int lanes_ahead(double v, int id) {
   }
 }
 
-template <bool kBF16, int V, bool kByLogit, bool kGrouped>
+// KT: top K known when compiled, or 0.
+template <bool kBF16, int V, bool kByLogit, bool kGrouped, int KT>
 __global__ __launch_bounds__(64 * kRouteWaves) void k_route_rows(RouteArgs a, int quads) {
+  const int K = KT ? KT : a.K;
   constexpr int L = V < 8 ? V : 8;  // length of a lane's list
   constexpr int VE = (V + 3) / 4;
   constexpr bool kWholeId = kBF16 && kByLogit;
@@ -335,20 +339,25 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_rows(RouteArgs a, in
                                  : (kIdBits <= 4 ? 0x1p-17f : 0x1p-16f);
   const float tol_group = a.sigmoid ? 0x1p-20f : 0x1p-15f;  // no keys yet
   constexpr float kTiny = 0x1p-100f;  // below it the places in the keys count
+  const bool whole = V % 4 == 0 && a.E == 16 * V;
   float b[V], bmax = 0.0f;
+  // no lane without experts, no bias that is not a number (by logits alone
+  // the masks cost less than the test for them)
+  bool plain = whole && !kByLogit;
   if constexpr (!kByLogit) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       b[i] = a.bias && e0 + i < a.E ? a.bias[e0 + i] : 0.0f;
       if (masks(b[i])) b[i] = -INFINITY;
       if (fabsf(b[i]) < INFINITY) bmax = fmaxf(bmax, fabsf(b[i]));
+      else plain = false;
     }
     bmax = row_max_f32(bmax);
+    plain = ballot64(!plain) == 0;
   }
   // Logits of quad w; rows past the last token repeat it (and store nothing).
   // Those of the next quad are fetched while the rounds of one run.
   float c[V];
-  const bool whole = V % 4 == 0 && a.E == 16 * V;
   auto fetch = [&](int w) {
     const size_t i = (size_t)min(w * 4 + row, a.N - 1) * a.E + e0;
     if (whole) {
@@ -371,37 +380,54 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_rows(RouteArgs a, in
     const int t = min(w * 4 + row, a.N - 1);
     const size_t at = (size_t)t * a.E;
     float mx = -INFINITY, z = 0.0f;
+    int k[V];
+    // choice values and their keys; kMasks: some may be masked or infinite
+    auto score = [&](auto masks_) {
+      constexpr bool kMasks = decltype(masks_)::value;
+      if constexpr (kMasks) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) c[i] = c[i] > -INFINITY ? c[i] : -INFINITY;  // NaN masks too
-    if (!a.sigmoid && (!kByLogit || !a.renorm)) {
+        for (int i = 0; i < V; ++i) c[i] = c[i] > -INFINITY ? c[i] : -INFINITY;  // NaN masks too
+      }
+      if (!a.sigmoid && (!kByLogit || !a.renorm)) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) mx = fmaxf(mx, c[i]);
-      mx = row_max_f32(mx);
+        for (int i = 0; i < V; ++i) mx = fmaxf(mx, c[i]);
+        mx = row_max_f32(mx);
 #pragma unroll
-      for (int i = 0; i < V; ++i) z += __builtin_amdgcn_exp2f((c[i] - mx) * kLog2e);
-      z = row_sum_f32(z);
-    }
-    if constexpr (!kByLogit) {
-      if (a.sigmoid) {
+        for (int i = 0; i < V; ++i) z += __builtin_amdgcn_exp2f((c[i] - mx) * kLog2e);
+        z = row_sum_f32(z);
+      }
+      if constexpr (!kByLogit) {
+        if (a.sigmoid) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-c[i] * kLog2e));
-          c[i] = c[i] > -INFINITY ? s + b[i] : -INFINITY;
-        }
-      } else {
-        const float rz = 1.0f / z;
+          for (int i = 0; i < V; ++i) {
+            const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-c[i] * kLog2e));
+            c[i] = !kMasks || c[i] > -INFINITY ? s + b[i] : -INFINITY;
+          }
+        } else {
+          const float rz = 1.0f / z;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float s = __builtin_amdgcn_exp2f((c[i] - mx) * kLog2e) * rz;
-          c[i] = c[i] > -INFINITY ? s + b[i] : -INFINITY;
+          for (int i = 0; i < V; ++i) {
+            const float s = __builtin_amdgcn_exp2f((c[i] - mx) * kLog2e) * rz;
+            c[i] = !kMasks || c[i] > -INFINITY ? s + b[i] : -INFINITY;
+          }
         }
       }
-    }
-    bool again = !(mx < INFINITY) || (!a.sigmoid && !(z < INFINITY));
-    int k[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i)  // + 0: one zero, whatever its sign
-      k[i] = sortable(__builtin_amdgcn_fmed3f(c[i] + 0.0f, -kHuge, kHuge));
+      for (int i = 0; i < V; ++i) {
+        const float v = c[i] + 0.0f;  // one zero, whatever its sign
+        k[i] = sortable(kMasks ? __builtin_amdgcn_fmed3f(v, -kHuge, kHuge) : v);
+      }
+    };
+    float probe = 0.0f;  // NaN if a logit is no number
+    if (plain) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) probe = fmaf(c[i], 0.0f, probe);
+    }
+    if (plain && ballot64(probe != probe) == 0)
+      score(std::false_type());
+    else
+      score(std::true_type());
+    bool again = !(mx < INFINITY) || (!a.sigmoid && !(z < INFINITY));
     bool open = true;
     if constexpr (kGrouped) {
       const int lanes = a.E / a.G / V;  // of a group: 1, 2, 4 or 8
@@ -421,7 +447,11 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_rows(RouteArgs a, in
       const float f1 = unsortable(t1), f2 = unsortable(t2);
       // with a masked second best the sum is -inf
       const float gs = a.group_top == 1 ? f1 : f2 > -kHuge ? f1 + f2 : -kHuge;
-      open = lanes_above<1>(gs) < a.top_groups * lanes;
+      const int above = lanes == 1   ? groups_above<1>(gs)
+                        : lanes == 2 ? groups_above<2>(gs)
+                        : lanes == 4 ? groups_above<4>(gs)
+                                     : groups_above<8>(gs);
+      open = above < a.top_groups;
       const uint32_t seg = (uint32_t)(ballot64(open) >> (row * 16)) & 0xffffu;
       const int gk = sortable(gs);
       const float low = unsortable(~row_max_i32(open ? ~gk : INT32_MIN));
@@ -438,7 +468,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_rows(RouteArgs a, in
         k[i] = (k[i] & ~0xffff) | (0xffff - (e0 + i));
       else
         k[i] = (k[i] & ~kIdMask) | (kIdMask - i);
-      if (!open || e0 + i >= a.E) k[i] = INT32_MIN;
+      if (!whole && e0 + i >= a.E) k[i] = INT32_MIN;
     }
     if (w + stride < quads) fetch(w + stride);
     if constexpr (V <= 8) {
@@ -449,10 +479,13 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_rows(RouteArgs a, in
 #pragma unroll
       for (int i = 8; i < V; i += 8) merge8(k, k + i);
     }
+    if constexpr (kGrouped) {
+#pragma unroll
+      for (int i = 0; i < L; ++i) k[i] = choose(open, k[i], INT32_MIN);
+    }
     // round j: lane j notes the j-th largest key and the lane it came from
     int mine = INT32_MIN, from = 0, taken = 0;
-    const int rounds = kWholeId ? a.K : a.K + 2;
-    for (int j = 0; j < rounds; ++j) {
+    auto round = [&](int j) {
       const int m = row_max_i32(k[0]);
       bool win = k[0] == m;
       if constexpr (!kWholeId) {
@@ -465,36 +498,43 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_rows(RouteArgs a, in
 #pragma unroll
       for (int i = 0; i + 1 < L; ++i) k[i] = choose(win, k[i + 1], k[i]);
       k[L - 1] = choose(win, INT32_MIN, k[L - 1]);
+    };
+    if constexpr (KT > 0) {
+#pragma unroll
+      for (int j = 0; j < (kWholeId ? KT : KT + 2); ++j) round(j);
+    } else {
+      const int rounds = kWholeId ? K : K + 2;
+      for (int j = 0; j < rounds; ++j) round(j);
     }
     const float value = unsortable(mine);
-    again |= (V > L && taken >= L) || (q < a.K && !(fabsf(value) < 0.99f * kHuge));
+    again |= (V > L && taken >= L) || (q < K && !(fabsf(value) < 0.99f * kHuge));
     int id = 0;
     if constexpr (kWholeId) {
-      if (q < a.K) id = 0xffff - (mine & 0xffff);
+      if (q < K) id = 0xffff - (mine & 0xffff);
     } else {
-      if (q <= a.K && mine != INT32_MIN) id = from * V + kIdMask - (mine & kIdMask);
+      if (q <= K && mine != INT32_MIN) id = from * V + kIdMask - (mine & kIdMask);
       // Neighbours too close to tell apart, among the first K + 1: those are
       // put in order by their exact values, unless more may belong with them.
       // (NaN stands for no key at all: nothing is close to it.)
       const float next = unsortable(dpp_i32<0x101>(mine));  // row_shl 1
-      const bool close = q <= a.K && value - next <= tol * (fabsf(value) + bmax + kTiny);
+      const bool close = q <= K && value - next <= tol * (fabsf(value) + bmax + kTiny);
       const uint32_t seg = (uint32_t)(ballot64(close) >> (row * 16)) & 0xffffu;
-      const bool near = (seg & ((1u << a.K) - 1u)) != 0;
-      again |= near && (((seg >> (a.K - 1)) & 3u) == 3u || (!kByLogit && !a.sigmoid));
+      const bool near = (seg & ((1u << K) - 1u)) != 0;
+      again |= near && (((seg >> (K - 1)) & 3u) == 3u || (!kByLogit && !a.sigmoid));
       if (ballot64(near && !again) != 0) {
         double d = -INFINITY;
-        int key = q <= a.K ? id : a.E + q;
-        if (q <= a.K && value > -0.99f * kHuge) {
+        int key = q <= K ? id : a.E + q;
+        if (q <= K && value > -0.99f * kHuge) {
           d = load_logit<kBF16>(a.logits, at + id);
           if constexpr (!kByLogit) d = 1.0 / (1.0 + exp(-d)) + (a.bias ? (double)a.bias[id] : 0.0);
         }
         const int place = lanes_ahead<1>(d, key);
         const int moved = __builtin_amdgcn_ds_permute((row * 16 + place) * 4, id);
-        if (q < a.K) id = moved;
+        if (q < K) id = moved;
       }
     }
     const uint64_t redo = ballot64(again);
-    const bool ours = q < a.K && !((redo >> (row * 16)) & 0xffffu);
+    const bool ours = q < K && !((redo >> (row * 16)) & 0xffffu);
     if (!ours) id = 0;
     const float l = load_logit<kBF16>(a.logits, at + id);
     float e, norm = 1.0f;
@@ -508,8 +548,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_rows(RouteArgs a, in
     }
     if (a.renorm) norm = row_sum_f32(ours ? e : 0.0f);
     if (ours && w * 4 + row < a.N) {
-      a.ids[(size_t)t * a.K + q] = id;
-      a.w[(size_t)t * a.K + q] = e / norm * a.scale;
+      a.ids[(size_t)t * K + q] = id;
+      a.w[(size_t)t * K + q] = e / norm * a.scale;
     }
     for (uint64_t left = redo; left;) {
       const int r = __builtin_ctzll(left) >> 4;
@@ -534,17 +574,22 @@ bool launch_rows(const RouteArgs& a, hipStream_t st) {
   if (!rows_fit(a, V, grouped)) return false;
   const int quads = (a.N + 3) / 4;
   const dim3 grid(min((quads + kRouteWaves - 1) / kRouteWaves, kRouteGroups)), block(64 * kRouteWaves);
+#define MB_R(L, G)                                                                               \
+  do {                                                                                           \
+    if (a.K == 8 && V >= 8 && !L)                                                                \
+      hipLaunchKernelGGL((k_route_rows<kBF16, V, L, G, V >= 8 && !L ? 8 : 0>), grid, block, 0,   \
+                         st, a, quads);                                                          \
+    else                                                                                         \
+      hipLaunchKernelGGL((k_route_rows<kBF16, V, L, G, 0>), grid, block, 0, st, a, quads);       \
+  } while (0)
   if (by_logit) {
-    if (grouped)
-      hipLaunchKernelGGL((k_route_rows<kBF16, V, true, true>), grid, block, 0, st, a, quads);
-    else
-      hipLaunchKernelGGL((k_route_rows<kBF16, V, true, false>), grid, block, 0, st, a, quads);
+    if (grouped) MB_R(true, true);
+    else MB_R(true, false);
   } else {
-    if (grouped)
-      hipLaunchKernelGGL((k_route_rows<kBF16, V, false, true>), grid, block, 0, st, a, quads);
-    else
-      hipLaunchKernelGGL((k_route_rows<kBF16, V, false, false>), grid, block, 0, st, a, quads);
+    if (grouped) MB_R(false, true);
+    else MB_R(false, false);
   }
+#undef MB_R
   return true;
 }
 
