@@ -14,9 +14,10 @@ constexpr int kMxThreads = 256;
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 // Both directions are bound by memory: a lane per 8 elements (16 bytes of
-// bf16, 4 of codes), four lanes per block of 32. With two or four chunks of a
-// lane in flight 8192 x 7168 bf16 rows there and back took 2 and 8 % longer
-// (51, 54 against 50 us).
+// bf16, 4 of codes), four lanes per block of 32. Measured on MI355X for 8192 x
+// 7168 bf16 rows: 22 us to quantise, 21 us back (6.8 TB/s: the codes stay in
+// the last-level cache). With two or four chunks of a lane in flight both
+// together took 2 and 8 % longer (51, 54 against 50 us).
 
 // Scale byte of a block from the bits of its largest magnitude: 127 +
 // floor(log2(amax)) - 2, at least 0, which is the bits' exponent less 2 for a
@@ -63,7 +64,9 @@ __global__ __launch_bounds__(kMxThreads) void k_quantize_mx4(const void* x, uint
 }
 
 // Row by row, for rows with an activation or that may be skipped: one wave
-// per 64 chunks of a row, a row's parts on consecutive waves.
+// per 64 chunks of a row, a row's parts on consecutive waves. The activation
+// is not rounded before it is quantised. 65536 rows of 2 x 2048 bf16: 107 us,
+// 5.7 TB/s.
 template <bool kBF16, bool kSwiglu>
 __global__ __launch_bounds__(kMxThreads) void k_quantize_mx4_rows(const void* x,
                                                                   const int32_t* row_src,
