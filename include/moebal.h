@@ -14,6 +14,11 @@
  *   mb_combine   weighted gather-reduce of the K expert-output rows of each
  *                token back into token order.
  *
+ * Around them: mb_route makes the ids and weights from the router's logits,
+ * mb_rmsnorm_fp8 and mb_quantize_mx4 the 8- and 4-bit rows to dispatch, and
+ * mb_expert_mx4 multiplies the dispatched 4-bit rows by their experts'
+ * weights.
+ *
  * The P logical ranks of the expert-parallel group are partitions of one
  * GPU's memory: rank r owns rows [r*cap, (r+1)*cap) of every [P*cap, ...]
  * buffer.
