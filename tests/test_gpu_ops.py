@@ -83,7 +83,10 @@ ROUTES = [  # N, E, K, groups, top_groups, group_top
     (301, 60, 4, 1, 1, 1), (301, 64, 6, 8, 3, 1), (130, 100, 10, 4, 2, 2), (130, 128, 8, 1, 1, 1),
     (258, 160, 6, 8, 3, 1), (1031, 256, 8, 8, 4, 2), (513, 256, 8, 1, 1, 1), (203, 384, 8, 1, 1, 1),
     (203, 384, 8, 8, 4, 2), (99, 320, 9, 16, 5, 2), (40, 512, 16, 64, 9, 2), (33, 1024, 32, 1, 1, 1),
-    (33, 1024, 32, 2, 1, 2), (5, 999, 7, 3, 2, 1),
+    (33, 1024, 32, 2, 1, 2), (5, 999, 7, 3, 2, 1), (70, 512, 8, 8, 4, 2), (70, 512, 14, 1, 1, 1),
+    (70, 512, 15, 1, 1, 1), (41, 128, 8, 8, 4, 2), (41, 64, 8, 16, 8, 2), (41, 256, 8, 2, 1, 1),
+    (41, 256, 8, 4, 2, 2), (41, 384, 8, 16, 3, 2), (41, 200, 8, 1, 1, 1), (41, 48, 8, 1, 1, 1),
+    (41, 130, 8, 1, 1, 1), (41, 16, 14, 1, 1, 1), (41, 16, 16, 1, 1, 1),
 ]
 
 
@@ -581,6 +584,68 @@ def test_expert_two_streams_at_once():
     torch.cuda.synchronize()
     a.check(ya)
     b.check(yb)
+
+
+# ------------------------------------------------------ offsets past 32 bits
+
+def test_route_of_many_tokens():
+    """More than 2^31 logits: the last tokens as in a batch of their own."""
+    n, e, k = (1 << 23) + 777, 260, 6
+    l = torch.empty(n, e, dtype=torch.bfloat16, device=G.dev()).normal_()
+    ids = torch.full((n, k), -1, dtype=torch.int32, device=G.dev())
+    w = torch.zeros(n, k, device=G.dev())
+    mb.route(mb.RouteParams.make(n, e, k, dtype="bf16"), l, ids, w)
+    tail = l[-500:].clone()
+    ids2, w2 = torch.empty_like(ids[:500]), torch.empty_like(w[:500])
+    mb.route(mb.RouteParams.make(500, e, k, dtype="bf16"), tail, ids2, w2)
+    assert torch.equal(ids[-500:], ids2) and torch.equal(w[-500:], w2)
+    want, _ = R.route(f64(tail[-50:]), k)
+    assert np.array_equal(ids[-50:].cpu().numpy(), want)
+
+
+def test_norm_and_4_bit_rows_past_32_bits():
+    n, h = 290_003, 7680  # 2.2e9 elements
+    x = torch.empty(n, h, dtype=torch.bfloat16, device=G.dev()).normal_()
+    w = torch.ones(h, dtype=torch.bfloat16, device=G.dev())
+    q = torch.empty(n, h, dtype=torch.uint8, device=G.dev())
+    qs = torch.empty(n, h // 128, device=G.dev())
+    y = torch.empty_like(x)
+    mb.rmsnorm_fp8(x, w, 1e-6, q, qs, residual=x, residual_out=y)
+    tail = x[-300:].clone()
+    q2, qs2, y2 = torch.empty_like(q[:300]), torch.empty_like(qs[:300]), torch.empty_like(tail)
+    mb.rmsnorm_fp8(tail, w, 1e-6, q2, qs2, residual=tail, residual_out=y2)
+    assert torch.equal(q[-300:], q2) and torch.equal(qs[-300:], qs2) and torch.equal(y[-300:], y2)
+    assert torch.equal(y2, 2 * tail)
+    c = q.view(-1)[: n * h // 2].view(n, h // 2)
+    s = torch.empty(n, h // 32, dtype=torch.uint8, device=G.dev())
+    mb.quantize_mx4(x, c, s)
+    mb.dequantize_mx4(c, s, y)
+    for at in (0, n // 2, n - 3):
+        v = f64(x[at:at + 3])
+        ws = R.mx4_scale_bytes(v)
+        assert np.array_equal(f64(y[at:at + 3]), R.mx4_values(R.pack4(R.mx4_codes(v, ws)), ws))
+
+
+@pytest.mark.parametrize("tokens", [64, 1 << 20])
+def test_expert_rows_past_32_bits(tokens):
+    """Rows and outputs of more than 2^32 bytes, by each way to the product."""
+    n, k, cap = 2048, 7168, 1_200_003
+    cu = np.array([[0, cap]], np.int32)
+    p = Product(1, 1, 1, 0, 4, n, k, tokens=tokens, plan=(cu, np.full((1, 1), -1, np.int32)))
+    p.dims = mb.Dims.make(tokens, 1, 1, 1, 0, 128, cap=cap)
+    if tokens == 64:  # this many rows in tiles of 16 take long: the last ones alone
+        p.bufs.cu_seqlens.copy_(torch.tensor([[cap - 700, cap]], dtype=torch.int32))
+    p.bufs.row_src = torch.empty(cap, dtype=torch.int32, device=G.dev())
+    p.dev[0] = torch.randint(0, 256, (cap, k // 2), dtype=torch.uint8, device=G.dev())
+    p.dev[1] = torch.randint(124, 130, (cap, k // 32), dtype=torch.uint8, device=G.dev())
+    y = torch.full((cap, n), -77.0, dtype=torch.bfloat16, device=G.dev())
+    p.run(y)
+    a = R.mx4_values(p.dev[0][-40:].cpu().numpy(), p.dev[1][-40:].cpu().numpy())
+    w = R.mx4_values(p.w, p.w_s)
+    want, mag = a @ w.T, np.abs(a) @ np.abs(w).T
+    err = np.abs(f64(y[-40:]) - want)
+    assert np.all(err <= k * 2.0**-23 * mag + 2.0**-8 * np.abs(want) + 1e-30)
+    assert (y[:100] == -77).all() == (tokens == 64)
 
 
 # -------------------------------------------------------------- a whole layer

@@ -227,7 +227,8 @@ def _speeds(dims: "Dims", speeds):
 
 
 def _dims_key(dims: "Dims") -> tuple:
-    return tuple(getattr(dims, n) for n, _ in Dims._fields_)
+    return (dims.n_tokens, dims.top_k, dims.n_experts, dims.n_ranks, dims.slots_per_rank,
+            dims.hidden, dims.cap, dims.dtype_in, dims.dtype_out)
 
 
 # handle of a device's current stream, without a Stream object for it (1.5 us
@@ -294,14 +295,15 @@ class PlanBuffers:
     def c_struct(self, dims: Dims | None = None) -> _PlanBufsC:
         """The mb_plan_bufs of these tensors; with `dims`, checked against
         them first (once per set of pointers and sizes)."""
-        ts = [getattr(self, n) for n, _ in _PlanBufsC._fields_]
-        ptrs = tuple(t.data_ptr() for t in ts)
+        ts = (self.counts, self.load_pre, self.load_post, self.rep_expert, self.slot_quota,
+              self.cu_seqlens, self.pos, self.row_src, self.status)
+        ptrs = tuple([t.data_ptr() for t in ts])
         if dims is None:
             return self._c if self._key is not None and self._key[0] == ptrs else _PlanBufsC(*ptrs)
         # the key holds the sizes too: a smaller tensor at the same address
         # is checked again
-        key = (ptrs, _dims_key(dims), tuple(t.numel() for t in ts),
-               tuple(t.is_contiguous() for t in ts))
+        key = (ptrs, _dims_key(dims), tuple([t.numel() for t in ts]),
+               tuple([t.is_contiguous() for t in ts]))
         if key != self._key:
             self.check(dims)
             self._c, self._key = _PlanBufsC(*ptrs), key
