@@ -222,7 +222,7 @@ struct alignas(16) TileLds {
   uint8_t w[2][kTileN * 128];
   uint8_t a[2][64 * JT * 128];
   uint8_t ws[2][kTileN * 16];
-  uint8_t as[2][kTileN * 16];  // 64 JT rows, copied by four waves: twice over when JT = 2
+  uint8_t as[2][kTileN * 16];  // 64 JT rows, and what the other waves copy
   uint8_t none[kTileN * 16];   // zeros: where copies of nothing go, the scales behind a row
   int first[kMaxPlanSlots + 1];
   int part[kExpertThreads / 64];
@@ -276,7 +276,9 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
     cut_a[j] = ((lane ^ (j << 2)) & 4) ? 0x80000000u : 0u;
   }
   const uint32_t cut_w = ((lane ^ crow) & 4) ? 0x80000000u : 0u;
-  const uint32_t csw = (wave * 64 + lane) * ks, csa = (wave * 64 + lane) % BM * ks;
+  // scales: a lane a row; none (zeros) past the tile's rows when JT = 2
+  const uint32_t csw = (wave * 64 + lane) * ks;
+  const uint32_t csa = wave * 64 < BM ? csw : 0x80000000u;
 
   // the copies' place in the sequence of pairs: two ahead of the product.
   // Past the last tile its last pair is copied again, unused.
