@@ -332,13 +332,13 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
   i32x4 fw[4][2], fa[JT][2];
   int sw[4], sa[JT];
   const int rn = (r & 19) | ((r & 4) << 1) | ((r & 8) >> 1);  // swap23
-  const int ow = (hn * 128 + rn) * 128, oa = (hm * 32 * JT + r) * 128;
+  const int ow = (hn * 128 + rn) * 128, oa = (hm * 32 + r) * 128;
   const int piece = ((2 * h) ^ ((r >> 1) & 7)) << 4;  // of (step 0, h, 0)
   auto read_w = [&](int buf, int step, int t, int u) {
     fw[t][u] = load16(lds.w[buf] + ow + (piece ^ (step * 64 + u * 16)) + t * 32 * 128);
   };
   auto read_a = [&](int buf, int step, int t, int u) {
-    fa[t][u] = load16(lds.a[buf] + oa + (piece ^ (step * 64 + u * 16)) + t * 32 * 128);
+    fa[t][u] = load16(lds.a[buf] + oa + (piece ^ (step * 64 + u * 16)) + t * 64 * 128);
   };
   // the two scales of a step (0..3 of its group), all rows at s
   auto scales = [&](const uint8_t* s, int row, int step) {
@@ -368,10 +368,15 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
 #pragma unroll
   for (int t = 0; t < JH; ++t) {
     read_a(0, 0, t, 0), read_a(0, 0, t, 1);
-    sa[t] = scales(lds.as[0], (hm * JT + t) * 32 + r, 0);
+    sa[t] = scales(lds.as[0], (2 * t + hm) * 32 + r, 0);
   }
-  for (int it = 0; it < tiles; ++it) {
-    f32x16 acc[4][JT] = {};
+  // A tile of no more than half its rows (a slot's last) leaves the second
+  // half of every wave's accumulators out, the waves' row tiles taking turns:
+  // their products are skipped (65536 rows over 320 slots, 2048 x 7168: 4 %).
+  auto run = [&](int it, auto half_) {
+    constexpr bool kHalf = decltype(half_)::value;
+    constexpr int JN = kHalf ? JH : JT;
+    f32x16 acc[4][JN] = {};
     Tile tile = next;
     for (int s = 0; s < pairs; ++s) {
       if (ahead == pairs) {  // at the end of the last pair but two
@@ -394,8 +399,8 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
 #pragma unroll
           for (int j = 0; j < JH; ++j)
             acc[i][j] = mfma_mx4(fw[i][u], fa[j][u], acc[i][j], sw[i], sa[j], u);
-          if (c < JT) read_a(buf, e, JH + (c >> 1), c & 1);
-          if (c < JH) sa[JH + c] = scales(as, (hm * JT + JH + c) * 32 + r, gs + e);
+          if (!kHalf && c < JT) read_a(buf, e, JH + (c >> 1), c & 1);
+          if (!kHalf && c < JH) sa[JH + c] = scales(as, (2 * (JH + c) + hm) * 32 + r, gs + e);
           if (e) copy_w(ahead, c);
           if (!e && c < 2) copy_scales(c);
           __builtin_amdgcn_sched_barrier(0);
@@ -417,12 +422,12 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
         for (int c = 0; c < 8; ++c) {
           const int u = c >> 2, i = c & 3;
 #pragma unroll
-          for (int j = JH; j < JT; ++j)
+          for (int j = JH; j < JN; ++j)
             acc[i][j] = mfma_mx4(fw[i][u], fa[j][u], acc[i][j], sw[i], sa[j], u);
           read_w(buf, 1 - e, i, u);
           if (u) sw[i] = scales(nws, hn * 128 + i * 32 + rn, ns);
           if (c < JT) read_a(buf, 1 - e, c >> 1, c & 1);
-          if (c < JH) sa[c] = scales(nas, (hm * JT + c) * 32 + r, ns);
+          if (c < JH) sa[c] = scales(nas, (2 * c + hm) * 32 + r, ns);
           if (e) {
 #pragma unroll
             for (int d = c * JT / 4; d < (c + 1) * JT / 4; ++d) copy_a(ahead, d);
@@ -436,8 +441,8 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
       c_buf ^= 1;
     }
 #pragma unroll
-    for (int j = 0; j < JT; ++j) {
-      const int m = tile.m0 + (hm * JT + j) * 32 + r;
+    for (int j = 0; j < JN; ++j) {
+      const int m = tile.m0 + (2 * j + hm) * 32 + r;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
 #pragma unroll
@@ -452,6 +457,12 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
       }
       __builtin_amdgcn_sched_barrier(0);  // one row of accumulators at a time: no spills
     }
+  };
+  for (int it = 0; it < tiles; ++it) {
+    if (next.hi - next.m0 > BM / 2)  // of tile `it`: the copies are two pairs ahead at most
+      run(it, std::false_type());
+    else
+      run(it, std::true_type());
   }
   // no copy may reach LDS after the workgroup has given it back
   wait_barrier<0>();
