@@ -544,16 +544,18 @@ __global__ __launch_bounds__(kExpertThreads) void k_expert_few(ExpertArgs p) {
 }
 
 // Which kernel, from the rows expected in a slot. Measured on MI355X, us, for
-// k_expert_few<1>, k_expert_few<4>, 128-row and 256-row tiles:
-//   320 slots, 7168 x 2048:   2 rows 350, 539, 358, 447; 8 rows 540, 721, 429,
-//     517; 32 rows 1266, 1259, 462, 556; 128 rows -, -, 695, 681; 256 rows
-//     -, -, 1055, 963; 512 rows -, -, 1827, 1529
-//   16 slots, 4096 x 4096:    8 rows 36, 55, 26, 33; 256 rows -, -, 66, 71
-//   9 slots, 2048 x 2048:     8 rows 11, 11, 15, 18; 32 rows 16, 17, 16, 20;
-//     256 rows -, -, 19, 25
-//   144 slots, 256 x 2048:    16 rows 23, 26; 64 rows 53, 46; 256 rows 179, 129
+// k_expert_few<1>, k_expert_few<4>, 128-row and 256-row tiles (weights n x k):
+//   320 slots, 2048 x 7168:   2 rows 332, 526, 335, 370; 8 rows 538, 716, 411,
+//     452; 32 rows 1258, 1260, 449, 485; 128 rows 4405, 3210, 666, 653; 256 rows
+//     8616, 6035, 1014, 921; 512 rows 17023, 11678, 1762, 1465
+//   16 slots, 4096 x 4096:    2 rows 27, 42, 26, 27; 8 rows 35, 53, 26, 27; 128
+//     rows 297, 206, 49, 37; 256 rows 571, 394, 67, 69; 512 rows 1126, 743, 107, 101
+//   9 slots, 2048 x 2048:     8 rows 11, 11, 14, 16; 32 rows 16, 17, 16, 17; 256
+//     rows 79, 56, 19, 25; 512 rows 149, 102, 28, 27
+//   144 slots, 2048 x 256:    16 rows 23, 26; 32 rows 33, 32; 256 rows 179, 130
 // So the tiles need enough of them to occupy the CUs, and k of two pairs of
-// steps; 128 rows to a tile waste less of it, 256 copy less.
+// steps; 128 rows to a tile waste less of it, 256 copy less. Near a whole number
+// of tiles per CU the rule can miss the better one (16 slots at 128 rows: 49, not 37).
 template <bool kBF16>
 void launch_expert_t(const ExpertArgs& p, int64_t rows, hipStream_t st) {
   const int64_t slots = (int64_t)p.P * p.NS, columns = (p.n + kTileN - 1) / kTileN;
