@@ -70,9 +70,17 @@ __global__ __launch_bounds__(kNormThreads) void k_rmsnorm_fp8(
       // 16 lanes of 8 elements share a block
       const float amax = __uint_as_float(row_max_u32(bits));
       const bool tiny = amax < 0x1p-110f;
-      const float scale = tiny ? 1.0f : amax * (1.0f / kE4m3Max);
-      const float f = tiny ? 0.0f : kE4m3Max / amax;
-      const uint2 o = {fp8x4(v[0], v[1], v[2], v[3], f), fp8x4(v[4], v[5], v[6], v[7], f)};
+      const float scale = tiny ? 1.0f : amax / kE4m3Max;
+      // y / scale as division rounds it: the product with the rounded
+      // reciprocal, less its remainder's (signs so that -0 stays -0)
+      const bool flat = tiny || amax == INFINITY;  // finite values give zeros
+      const float d = flat ? 0.0f : scale, f = flat ? 0.0f : 1.0f / scale;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float t = v[j] * f;
+        v[j] = fmaf(fmaf(t, d, -v[j]), -f, t);
+      }
+      const uint2 o = {fp8x4(v[0], v[1], v[2], v[3]), fp8x4(v[4], v[5], v[6], v[7])};
       reinterpret_cast<uint2*>(q)[row + c] = bad ? uint2{0x7f7f7f7fu, 0x7f7f7f7fu} : o;
       if ((threadIdx.x & 15) == 0) q_scale[(row + c) >> 4] = bad ? NAN : scale;
     }

@@ -54,11 +54,11 @@ __device__ __forceinline__ void store8(void* p, size_t c, const float* v) {
   }
 }
 
-// Four values times f as e4m3fn bytes, round to nearest even. |v * f| may
-// pass 448 by the rounding of f, never by half a step (16): no overflow.
-__device__ __forceinline__ uint32_t fp8x4(float a, float b, float c, float d, float f) {
-  int o = __builtin_amdgcn_cvt_pk_fp8_f32(a * f, b * f, 0, false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c * f, d * f, o, true);
+// Four values as e4m3fn bytes, round to nearest even. A quotient may pass 448
+// by its own rounding and its divisor's, never by half a step (16): no overflow.
+__device__ __forceinline__ uint32_t fp8x4(float a, float b, float c, float d) {
+  const int o = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, o, true);
 }
 
 }  // namespace mb
