@@ -45,3 +45,54 @@ def test_norm_codes_are_the_quotients(n, h):
     assert np.array_equal(qs.cpu().numpy(), scale)
     want = torch.from_numpy((yy / scale[:, :, None]).reshape(n, h)).to(torch.float8_e4m3fn)
     assert torch.equal(q.cpu(), want.view(torch.uint8))
+
+
+# ------------------------------------------------------------------- route
+
+def plain_choice(l, k, groups, top_groups, score, bias):
+    """The ids of all rows at once in 64 bits, group scores of two experts."""
+    l = l.astype(np.float64)
+    n, e = l.shape
+    if score == "sigmoid":
+        c = 1 / (1 + np.exp(-l))
+    else:
+        c = np.exp(l - l.max(axis=1, keepdims=True))
+        c /= c.sum(axis=1, keepdims=True)
+    c = c + bias.astype(np.float64)
+    g = np.sort(c.reshape(n, groups, -1), axis=2)[:, :, -2:].sum(axis=2)
+    first = np.argsort(-g, axis=1, kind="stable")[:, :top_groups]
+    closed = np.ones((n, groups), bool)
+    np.put_along_axis(closed, first, False, axis=1)
+    c[np.repeat(closed, e // groups, axis=1)] = -np.inf
+    return np.argsort(-c, axis=1, kind="stable")[:, :k]
+
+
+@pytest.mark.parametrize("e,k", [(64, 6), (256, 8)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("at", [-1.0, -8.0, -12.0, -25.0, -44.0, -60.0, -68.0, -80.0])
+def test_route_far_logits_in_groups(at, score, e, k):
+    """Scores far below one, close together: their binary32 values are off by
+    their logit's size, and what that leaves open is decided in binary64."""
+    n = 20000
+    r = rng(e, int(-at), len(score))
+    l = np.float32(at + 0.01 * r.uniform(-1, 1, (n, e)))
+    if score == "softmax":
+        l[:, 0] = 0.0
+    elif at == -44.0:  # two groups' sums, 8.532099599e-20 and 8.532099253e-20
+        s = e // 8
+        l[0] = -90.0
+        l[0, 0], l[0, 1] = -44.579517, -44.622982
+        l[0, s], l[0, s + 1] = -44.590237, -44.611908
+        l[0, 2 * s::s] = -40.0
+        l[0, 5 * s::s] = -90.0  # those two groups fight for the last open place
+    disabled = np.zeros(e, np.float32)
+    disabled[e - 1] = -1e9
+    prm = mb.RouteParams.make(n, e, k, score=score, n_groups=8, top_groups=4, group_top=2)
+    ids = torch.empty(n, k, dtype=torch.int32, device=G.dev())
+    w = torch.empty(n, k, device=G.dev())
+    x = dev(l)
+    for bias in (None, np.zeros(e, np.float32), disabled):
+        want = plain_choice(l, k, 8, 4, score, np.zeros(e) if bias is None else bias)
+        mb.route(prm, x, ids, w, bias=None if bias is None else dev(bias))
+        wrong = np.nonzero((ids.cpu().numpy() != want).any(axis=1))[0]
+        assert not len(wrong), (len(wrong), wrong[:5], ids[wrong[0]], want[wrong[0]])

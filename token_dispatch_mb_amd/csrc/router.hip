@@ -258,7 +258,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route(RouteArgs a) {
 // Bound by vector instructions (about 900 for a wave's four tokens of 256
 // experts: a third for scores and keys, a third for the rounds), not by the
 // 6.3 TB/s its reads could have. Measured on MI355X: 131072 tokens x 256
-// experts in 8 groups, fp32, sigmoid and bias: 63 us (2.2 TB/s; a wave per
+// experts in 8 groups, fp32, sigmoid and bias: 64 us (2.2 TB/s; a wave per
 // token in binary64 takes 355); without route_exact's rows, a few in 100000,
 // it would be 13 us less, their one long chain being the tail. 65536 x 384,
 // softmax: 29 us (3.5 TB/s). 8192 x 256, bf16: 11 us.
@@ -338,14 +338,19 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_rows(RouteArgs a, in
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane & 15, row = lane >> 4;
   const int e0 = q * V;
-  // How far rounding may move the difference of two choice values, relative to
-  // their magnitude and the largest bias: keys lose 2^-(23 - bits) twice,
-  // scores are off by 2^-22 each (softmax: by |l - max| 2^-23, and 0 below
-  // e^-87).
-  const float tol = kByLogit ? 0x1p-17f
-                    : !a.sigmoid ? 0x1p-15f
-                                 : (kIdBits <= 4 ? 0x1p-17f : 0x1p-16f);
-  const float tol_group = a.sigmoid ? 0x1p-20f : 0x1p-15f;  // no keys yet
+  // How far rounding may move a choice value, in units of 2^-24 (a product's
+  // rounding, relative). A score s: the products in front of the exponential
+  // are off by their own size, which is at most ln(1/s): 1.22 ln(1/s) with the
+  // constant's error, 2.22 for softmax, where the difference to the largest
+  // logit is rounded before; exponential, sum and reciprocal add 5 (the
+  // instructions' own errors stay below 2 each, measured), and 54 where the
+  // sum goes over a row (32 terms in line). s is unknown beside a
+  // bias: at most |choice| + |bias|, and 1. (s ln(1/s) rises with s up to 1/e;
+  // past it the constants cover it.) A choice value is rounded once more, and
+  // cut by the place in its key.
+  const float per_log2 = a.sigmoid ? 0.85f : 1.54f, fixed = a.sigmoid ? 5.0f : 54.0f;
+  constexpr float kUnit = 0x1.1p-24f;  // with room for products of two errors
+  constexpr float kKey = kWholeId ? 0.0f : (float)(2 << kIdBits);
   constexpr float kTiny = 0x1p-100f;  // below it the places in the keys count
   const bool whole = V % 4 == 0 && a.E == 16 * V;
   float b[V], bmax = 0.0f;
@@ -363,6 +368,11 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_rows(RouteArgs a, in
     bmax = row_max_f32(bmax);
     plain = ballot64(!plain) == 0;
   }
+  // the part of a score whose choice value is `v` in magnitude
+  auto score_error = [&](float v) {
+    const float most = fminf(v + bmax + kTiny, 1.0f);
+    return most * (per_log2 * (float)(127 - (int)(__float_as_uint(most) >> 23)) + fixed);
+  };
   // Logits of quad w; rows past the last token repeat it (and store nothing).
   // Those of the next quad are fetched while the rounds of one run.
   float c[V];
@@ -461,13 +471,19 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_rows(RouteArgs a, in
                                      : groups_above<8>(gs);
       open = above < a.top_groups;
       const uint32_t seg = (uint32_t)(ballot64(open) >> (row * 16)) & 0xffffu;
-      const int gk = sortable(gs);
-      const float low = unsortable(~row_max_i32(open ? ~gk : INT32_MIN));
-      const float high = unsortable(row_max_i32(open ? INT32_MIN : gk));
+      // what the exact score may be at least and at most (maxima of logits are exact)
+      float off = 0.0f;
+      if constexpr (!kByLogit) {
+        const bool two = a.group_top == 2;
+        const float sum = fabsf(f1) + (two ? fabsf(f2) : 0.0f);
+        off = two ? 2.0f * score_error(0.5f * sum) : score_error(sum);
+        off = kUnit * off + kUnit * sum + 2.0f * kUnit * fabsf(gs);
+      }
+      const float low = unsortable(~row_max_i32(open ? ~sortable(gs - off) : INT32_MIN));
+      const float high = unsortable(row_max_i32(open ? INT32_MIN : sortable(gs + off)));
       // unless exactly top_groups groups are ahead of the rest by more than
       // rounding, and their scores are numbers
-      again |= __popc(seg) != a.top_groups * lanes || !(fabsf(low) < 0.99f * kHuge) ||
-               !(low - high > (kByLogit ? 0.0f : tol_group * (fabsf(low) + 2 * bmax + kTiny)));
+      again |= __popc(seg) != a.top_groups * lanes || !(fabsf(low) < 0.99f * kHuge) || !(low > high);
     }
     // the low bits: larger for the lower id
 #pragma unroll
@@ -525,7 +541,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_rows(RouteArgs a, in
       // put in order by their exact values, unless more may belong with them.
       // (NaN stands for no key at all: nothing is close to it.)
       const float next = unsortable(dpp_i32<0x101>(mine));  // row_shl 1
-      const bool close = q <= K && value - next <= tol * (fabsf(value) + bmax + kTiny);
+      const float mag = fabsf(value), off = kByLogit ? 0.0f : score_error(mag);
+      const bool close = q <= K && value - next <= 2 * kUnit * (off + kKey * (mag + kTiny));
       const uint32_t seg = (uint32_t)(ballot64(close) >> (row * 16)) & 0xffffu;
       const bool near = (seg & ((1u << K) - 1u)) != 0;
       again |= near && (((seg >> (K - 1)) & 3u) == 3u || (!kByLogit && !a.sigmoid));
