@@ -501,7 +501,8 @@ int mb_dequantize_mx4(int32_t n_rows, int32_t hidden, int32_t dtype, const uint8
  *  y_dev        [P*cap, n_out] of dtype_out.
  * Reads plan->cu_seqlens, rep_expert and status; does nothing under a fatal
  * status. dims gives E, P, R, cap, N*K (the rows expected, which picks the
- * tile size) and dtype_out; hidden and dtype_in are not used. a, w and y
+ * tile size) and dtype_out; hidden and dtype_in are not used. P*cap is at most
+ * 2^31 - 256 here (rows up to a whole tile behind the last one are numbered). a, w and y
  * 16-byte aligned, the scales 4-byte.
  */
 int mb_expert_mx4(const mb_dims* dims, const mb_plan_bufs* plan, int32_t n_out, int32_t k_in,

@@ -404,6 +404,9 @@ int mb_expert_mx4(const mb_dims* dims, const mb_plan_bufs* plan, int32_t n_out, 
   if (!aligned16(a_dev) || !aligned16(w_dev) || !aligned16(y_dev) || !aligned4(a_scale_dev) ||
       !aligned4(w_scale_dev))
     return MB_ERR_INVALID_ARG;
+  // a tile's rows are numbered in int32, also those behind the last region's end
+  if ((int64_t)dims->n_ranks * dims->cap > INT32_MAX - (kMaxTileRows - 1))
+    return MB_ERR_INVALID_ARG;
   const Geometry g = geometry(*dims);
   // output tiles of at least 16 rows x 16 columns are numbered in int32
   const int64_t row_tiles = (int64_t)dims->n_ranks * dims->cap / 16 + (int64_t)dims->n_ranks * g.NS;

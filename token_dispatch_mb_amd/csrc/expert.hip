@@ -231,6 +231,7 @@ struct alignas(16) TileLds {
 template <bool kBF16, int JT>
 __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p) {
   constexpr int BM = 64 * JT, JH = JT / 2;
+  static_assert(BM <= kMaxTileRows, "rows behind a tile's last are numbered in int32");
   __shared__ TileLds<JT> lds;
   if (p.status[0] & MB_ST_FATAL) return;
   const int nslots = p.P * p.NS;

@@ -21,6 +21,7 @@ constexpr int kMaxSlots = 16;
 constexpr int kMaxGroups = 64;             // one wave lane per group in k_route
 constexpr int kMaxWaves = (1 << 26) - 16;  // waves of one launch: fewer than 2^32 threads
 constexpr int kMaxExpertDim = 1 << 20;     // n_out and k_in of the experts' products
+constexpr int kMaxTileRows = 256;          // rows of one of their tiles at most
 // Block-count tables k_plan and k_assign sum directly instead of running
 // k_scan: at most this many routing blocks per source and block counts.
 constexpr int kSmallTableBlocks = 4;
