@@ -203,14 +203,14 @@ __device__ __forceinline__ i32x4 buffer_of(const void* p, uint32_t bytes) {
                __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
 }
 
-// Copies 64 lanes' 16 or 4 bytes at buf[voff + soff] to consecutive places of
-// LDS from `to` (wave-uniform). No register is written. In assembly because
-// the compiler, for its builtin, waits for every copy in flight before the
-// next read of any LDS; the waits that order copies and reads are
-// wait_barrier's.
+// Copies 64 lanes' 16 bytes at buf[voff + soff] to consecutive places of LDS
+// from `to` (wave-uniform; the instruction takes it from m0, one instruction
+// after m0 was written). No register is written. In assembly because the
+// compiler, for its builtin, waits for every copy in flight before the next
+// read of any LDS; the waits that order copies and reads are wait_barrier's.
 __device__ __forceinline__ void copy16(i32x4 buf, lds_ptr to, uint32_t voff, uint32_t soff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-               ::"s"((uint32_t)(uintptr_t)to), "v"(voff), "s"(buf), "s"(soff)
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               ::"{m0}"((uint32_t)(uintptr_t)to), "v"(voff), "s"(buf), "s"(soff)
                : "memory");
 }
 struct Tile {
