@@ -423,7 +423,8 @@ typedef struct mb_route_params {
  *  ids_dev    [N*K] int32 out.
  *  w_dev      [N*K] fp32 out.
  * prm is host memory, read during the call only. logits must be 16-byte
- * aligned, the others 4-byte.
+ * aligned, the others 4-byte. The outputs overlap neither each other nor an
+ * input (refused).
  */
 int mb_route(const mb_route_params* prm, const void* logits_dev, const float* bias_dev,
              int32_t* ids_dev, float* w_dev, hipStream_t stream);
@@ -448,7 +449,8 @@ int mb_route(const mb_route_params* prm, const void* logits_dev, const float* bi
  *  residual_dev      [n_rows, H], or NULL: no addition.
  *  residual_out_dev  [n_rows, H] h rounded to dtype (round to nearest even);
  *                    NULL to not store it. May be x_dev or residual_dev
- *                    themselves (in place); no other overlap is allowed.
+ *                    themselves (in place); no other overlap is allowed
+ *                    (refused).
  *                    Needs residual_dev.
  *  y_dev             [n_rows, H] the normed rows in dtype, or NULL.
  *  q_dev             [n_rows, H] fp8 codes.
@@ -475,7 +477,8 @@ int mb_rmsnorm_fp8(int32_t n_rows, int32_t hidden, int32_t dtype, float eps, con
  *              padding rows of a plan's row_src) are not written.
  *  q_dev       [n_rows, hidden/2], q_scale_dev [n_rows, hidden/32].
  * hidden % 32 == 0, n_rows >= 0 and n_rows * ceil(hidden / 512) <= 2^26 - 16;
- * x and q 16-byte aligned, row_src 4-byte.
+ * x and q 16-byte aligned, row_src 4-byte. q and q_scale overlap neither each
+ * other nor an input (refused).
  */
 int mb_quantize_mx4(int32_t n_rows, int32_t hidden, int32_t dtype, int32_t act, const void* x_dev,
                     const int32_t* row_src_dev, uint8_t* q_dev, uint8_t* q_scale_dev,
@@ -483,7 +486,7 @@ int mb_quantize_mx4(int32_t n_rows, int32_t hidden, int32_t dtype, int32_t act, 
 
 /* The values of microscaled 4-bit rows, as rows of dtype (MB_F32 or MB_BF16;
  * both hold them exactly). A scale of 255 gives NaN. Layouts, limits and
- * alignment as mb_quantize_mx4. */
+ * alignment as mb_quantize_mx4; x overlaps no input (refused). */
 int mb_dequantize_mx4(int32_t n_rows, int32_t hidden, int32_t dtype, const uint8_t* q_dev,
                       const uint8_t* q_scale_dev, void* x_dev, hipStream_t stream);
 
@@ -503,7 +506,7 @@ int mb_dequantize_mx4(int32_t n_rows, int32_t hidden, int32_t dtype, const uint8
  * status. dims gives E, P, R, cap, N*K (the rows expected, which picks the
  * tile size) and dtype_out; hidden and dtype_in are not used. P*cap is at most
  * 2^31 - 256 here (rows up to a whole tile behind the last one are numbered). a, w and y
- * 16-byte aligned, the scales 4-byte.
+ * 16-byte aligned, the scales 4-byte; y overlaps no input (refused).
  */
 int mb_expert_mx4(const mb_dims* dims, const mb_plan_bufs* plan, int32_t n_out, int32_t k_in,
                   const uint8_t* a_dev, const uint8_t* a_scale_dev, const uint8_t* w_dev,

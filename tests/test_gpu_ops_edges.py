@@ -10,7 +10,7 @@ import token_dispatch_mb_amd as mb
 
 from . import gpu_harness as G
 from . import plain_ops as R
-from .test_gpu_ops import check_route, dev, f64, rng
+from .test_gpu_ops import Product, dev, rng
 
 pytestmark = pytest.mark.gpu
 
@@ -96,3 +96,48 @@ def test_route_far_logits_in_groups(at, score, e, k):
         mb.route(prm, x, ids, w, bias=None if bias is None else dev(bias))
         wrong = np.nonzero((ids.cpu().numpy() != want).any(axis=1))[0]
         assert not len(wrong), (len(wrong), wrong[:5], ids[wrong[0]], want[wrong[0]])
+
+
+# ---------------------------------------------------------------- overlaps
+
+def test_outputs_beside_their_inputs_and_over_them():
+    """Buffers that touch in one allocation are separate ones; outputs over
+    inputs are refused with the reason."""
+    g = G.dev()
+    mem = torch.zeros(1 << 16, dtype=torch.uint8, device=g)
+
+    def part(lo, n, dtype, *shape):
+        return mem[lo:lo + n].view(dtype).view(*shape)
+
+    x = torch.randn(4, 256, device=g)
+    part(0, 4096, torch.float32, 4, 256).copy_(x)
+    q, s = part(4096, 512, torch.uint8, 4, 128), part(4608, 32, torch.uint8, 4, 8)
+    mb.quantize_mx4(part(0, 4096, torch.float32, 4, 256), q, s)
+    q2, s2 = torch.empty_like(q), torch.empty_like(s)
+    mb.quantize_mx4(x, q2, s2)
+    assert torch.equal(q, q2) and torch.equal(s, s2)
+    back = part(4640, 2048, torch.bfloat16, 4, 256)
+    mb.dequantize_mx4(q, s, back)
+    assert torch.equal(q, q2) and torch.equal(s, s2)
+    with pytest.raises(ValueError, match="overlap"):
+        mb.quantize_mx4(part(0, 4096, torch.float32, 4, 256), part(4080, 512, torch.uint8, 4, 128),
+                        s)
+    with pytest.raises(ValueError, match="overlap"):
+        mb.dequantize_mx4(q, s, part(4624, 2048, torch.bfloat16, 4, 256))
+
+    prm = mb.RouteParams.make(16, 64, 4)
+    l = part(0, 4096, torch.float32, 16, 64)
+    l.normal_()
+    ids, w = part(4096, 256, torch.int32, 16, 4), part(4352, 256, torch.float32, 16, 4)
+    mb.route(prm, l, ids, w)
+    ids2, w2 = torch.empty_like(ids), torch.empty_like(w)
+    mb.route(prm, l, ids2, w2)
+    assert torch.equal(ids, ids2) and torch.equal(w, w2)
+    with pytest.raises(ValueError, match="overlap"):
+        mb.route(prm, l, part(4092, 256, torch.int32, 16, 4), w)
+
+    p = Product(21, 2, 2, 1, 20, 64, 128)
+    over = p.dev[2].view(-1)[:p.dims.rows * 64 * 2].view(torch.bfloat16).view(-1, 64)
+    with pytest.raises(ValueError, match="overlap"):
+        p.run(over)
+    p.check(p.run())

@@ -451,7 +451,9 @@ def route(prm: RouteParams, logits: torch.Tensor, ids: torch.Tensor, w: torch.Te
     rc = _lib.mb_route(ctypes.byref(prm), _ptr(logits), _ptr(bias), _ptr(ids), _ptr(w),
                        _stream(stream, logits, bias, ids, w))
     if rc != OK:
-        raise MoebalError("mb_route", rc)
+        _refused("mb_route", rc, (logits, n * prm.n_experts * logits.element_size(), False),
+                 (bias, 4 * prm.n_experts, False), (ids, 4 * n * prm.top_k, True),
+                 (w, 4 * n * prm.top_k, True))
 
 
 def _row_dtype(code: int) -> torch.dtype:
@@ -477,12 +479,21 @@ def _distinct(spans: list) -> None:
     end, written = 0, False
     for lo, hi, out in spans:
         if lo < end and hi > lo and (written or out):
-            raise ValueError("outputs must not overlap each other or the inputs (residual_out may "
-                             "be x or residual themselves)")
+            raise ValueError("outputs must not overlap each other or the inputs (but "
+                             "rmsnorm_fp8's residual_out may be its x or residual)")
         if hi > end:
             end, written = hi, out
         else:
             written |= out
+
+
+def _refused(fn: str, rc: int, *spans) -> None:
+    """Raise for a call the library refused: as a ValueError where it is for
+    outputs that overlap. `spans`: (tensor or None, bytes, is it written)."""
+    if rc == ERR_INVALID_ARG:
+        _distinct([(t.data_ptr(), t.data_ptr() + n, out) for t, n, out in spans
+                   if t is not None and n > 0])
+    raise MoebalError(fn, rc)
 
 
 def rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float, q: torch.Tensor,
@@ -547,7 +558,8 @@ def quantize_mx4(x: torch.Tensor, q: torch.Tensor, q_scale: torch.Tensor, act: s
     rc = _lib.mb_quantize_mx4(m, h, code, a, _ptr(x), _ptr(row_src), _ptr(q), _ptr(q_scale),
                               _stream(stream, x, row_src, q, q_scale))
     if rc != OK:
-        raise MoebalError("mb_quantize_mx4", rc)
+        _refused("mb_quantize_mx4", rc, (x, x.numel() * x.element_size(), False),
+                 (row_src, 4 * m, False), (q, m * (h // 2), True), (q_scale, m * (h // 32), True))
 
 
 def dequantize_mx4(q: torch.Tensor, q_scale: torch.Tensor, x: torch.Tensor, stream=None) -> None:
@@ -558,7 +570,8 @@ def dequantize_mx4(q: torch.Tensor, q_scale: torch.Tensor, x: torch.Tensor, stre
     rc = _lib.mb_dequantize_mx4(m, h, code, _ptr(q), _ptr(q_scale), _ptr(x),
                                 _stream(stream, q, q_scale, x))
     if rc != OK:
-        raise MoebalError("mb_dequantize_mx4", rc)
+        _refused("mb_dequantize_mx4", rc, (q, m * (h // 2), False),
+                 (q_scale, m * (h // 32), False), (x, x.numel() * x.element_size(), True))
 
 
 def expert_mx4(dims: Dims, bufs: PlanBuffers, n_out: int, k_in: int, a: torch.Tensor,
@@ -576,7 +589,12 @@ def expert_mx4(dims: Dims, bufs: PlanBuffers, n_out: int, k_in: int, a: torch.Te
                             _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), _ptr(y),
                             _stream(stream, a, a_scale, w, w_scale, y, bufs.status))
     if rc != OK:
-        raise MoebalError("mb_expert_mx4", rc)
+        rows, wide = dims.rows, dims.n_experts * n_out
+        _refused("mb_expert_mx4", rc, (a, rows * (k_in // 2), False),
+                 (a_scale, rows * (k_in // 32), False), (w, wide * (k_in // 2), False),
+                 (w_scale, wide * (k_in // 32), False), (y, rows * n_out * y.element_size(), True),
+                 *((t, t.numel() * 4, False) for t in (bufs.cu_seqlens, bufs.rep_expert,
+                                                       bufs.status)))
 
 
 def plan_status(bufs: PlanBuffers, stream=None):

@@ -92,6 +92,25 @@ static bool plan_ptrs_ok(const mb_dims* d, const mb_plan_bufs* o) {
 static bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 static bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
+// Memory a call reads, or writes.
+struct Span {
+  const void* at;
+  int64_t bytes;
+  bool written;
+};
+
+// No span that is written overlaps another: workgroups run in any order, so
+// one's output could be another's input.
+static bool outputs_apart(std::initializer_list<Span> spans) {
+  for (const Span* a = spans.begin(); a != spans.end(); ++a)
+    for (const Span* b = a + 1; b != spans.end(); ++b) {
+      if (!(a->written || b->written) || a->bytes <= 0 || b->bytes <= 0) continue;
+      const uintptr_t p = (uintptr_t)a->at, q = (uintptr_t)b->at;
+      if (p < q + (uint64_t)b->bytes && q < p + (uint64_t)a->bytes) return false;
+    }
+  return true;
+}
+
 extern "C" {
 
 int mb_version(void) { return MB_VERSION; }
@@ -333,6 +352,12 @@ int mb_route(const mb_route_params* prm, const void* logits_dev, const float* bi
   if (p.n_tokens > 0 && (!logits_dev || !ids_dev || !w_dev)) return MB_ERR_INVALID_ARG;
   if (!aligned16(logits_dev) || !aligned4(bias_dev) || !aligned4(ids_dev) || !aligned4(w_dev))
     return MB_ERR_INVALID_ARG;
+  const int64_t n = p.n_tokens, picks = n * p.top_k * 4;
+  if (!outputs_apart({{logits_dev, n * p.n_experts * elt_bytes(p.dtype), false},
+                      {bias_dev, n && bias_dev ? (int64_t)p.n_experts * 4 : 0, false},
+                      {ids_dev, picks, true},
+                      {w_dev, picks, true}}))
+    return MB_ERR_INVALID_ARG;
   return launch_route(p, logits_dev, bias_dev, ids_dev, w_dev, stream) == hipSuccess ? MB_OK
                                                                                      : MB_ERR_HIP;
 }
@@ -350,6 +375,18 @@ int mb_rmsnorm_fp8(int32_t n_rows, int32_t hidden, int32_t dtype, float eps, con
   if (!aligned16(x_dev) || !aligned16(residual_dev) || !aligned16(weight_dev) ||
       !aligned16(residual_out_dev) || !aligned16(y_dev) || !aligned16(q_dev) ||
       !aligned4(q_scale_dev))
+    return MB_ERR_INVALID_ARG;
+  // in place, the input's span is the written one
+  const int64_t elems = (int64_t)n_rows * hidden, rows = elems * elt_bytes(dtype);
+  const bool over_x = residual_out_dev && residual_out_dev == x_dev;
+  const bool over_res = residual_out_dev && residual_out_dev == residual_dev;
+  if (!outputs_apart({{x_dev, rows, over_x},
+                      {residual_dev, residual_dev && !(over_x && over_res) ? rows : 0, over_res},
+                      {residual_out_dev, residual_out_dev && !over_x && !over_res ? rows : 0, true},
+                      {weight_dev, n_rows ? hidden * elt_bytes(dtype) : 0, false},
+                      {y_dev, y_dev ? rows : 0, true},
+                      {q_dev, elems, true},
+                      {q_scale_dev, elems / 32, true}}))
     return MB_ERR_INVALID_ARG;
   return launch_rmsnorm_fp8(n_rows, hidden, dtype == MB_BF16, eps, x_dev, residual_dev, weight_dev,
                             residual_out_dev, y_dev, q_dev, q_scale_dev, stream) == hipSuccess
@@ -372,6 +409,12 @@ int mb_quantize_mx4(int32_t n_rows, int32_t hidden, int32_t dtype, int32_t act, 
   if (act != MB_ACT_NONE && act != MB_ACT_SWIGLU) return MB_ERR_INVALID_ARG;
   if (n_rows > 0 && (!x_dev || !q_dev || !q_scale_dev)) return MB_ERR_INVALID_ARG;
   if (!aligned16(x_dev) || !aligned16(q_dev) || !aligned4(row_src_dev)) return MB_ERR_INVALID_ARG;
+  const int64_t elems = (int64_t)n_rows * hidden;
+  if (!outputs_apart({{x_dev, elems * elt_bytes(dtype) * (act == MB_ACT_SWIGLU ? 2 : 1), false},
+                      {row_src_dev, row_src_dev ? (int64_t)n_rows * 4 : 0, false},
+                      {q_dev, elems / 2, true},
+                      {q_scale_dev, elems / 32, true}}))
+    return MB_ERR_INVALID_ARG;
   return launch_quantize_mx4(n_rows, hidden, dtype == MB_BF16, act == MB_ACT_SWIGLU, x_dev,
                              row_src_dev, q_dev, q_scale_dev, stream) == hipSuccess
              ? MB_OK
@@ -383,6 +426,11 @@ int mb_dequantize_mx4(int32_t n_rows, int32_t hidden, int32_t dtype, const uint8
   if (!mx4_rows_ok(n_rows, hidden, dtype)) return MB_ERR_INVALID_ARG;
   if (n_rows > 0 && (!x_dev || !q_dev || !q_scale_dev)) return MB_ERR_INVALID_ARG;
   if (!aligned16(x_dev) || !aligned16(q_dev)) return MB_ERR_INVALID_ARG;
+  const int64_t elems = (int64_t)n_rows * hidden;
+  if (!outputs_apart({{q_dev, elems / 2, false},
+                      {q_scale_dev, elems / 32, false},
+                      {x_dev, elems * elt_bytes(dtype), true}}))
+    return MB_ERR_INVALID_ARG;
   return launch_dequantize_mx4(n_rows, hidden, dtype == MB_BF16, q_dev, q_scale_dev, x_dev,
                                stream) == hipSuccess
              ? MB_OK
@@ -411,6 +459,17 @@ int mb_expert_mx4(const mb_dims* dims, const mb_plan_bufs* plan, int32_t n_out, 
   // output tiles of at least 16 rows x 16 columns are numbered in int32
   const int64_t row_tiles = (int64_t)dims->n_ranks * dims->cap / 16 + (int64_t)dims->n_ranks * g.NS;
   if (row_tiles * ((n_out + 15) / 16) > INT32_MAX) return MB_ERR_INVALID_ARG;
+  const int64_t rows = dims->n_tokens ? (int64_t)dims->n_ranks * dims->cap : 0;
+  const int64_t weights = (int64_t)dims->n_experts * n_out;
+  if (!outputs_apart({{y_dev, rows * n_out * elt_bytes(dims->dtype_out), true},
+                      {a_dev, rows * k_in / 2, false},
+                      {a_scale_dev, rows * k_in / 32, false},
+                      {w_dev, weights * k_in / 2, false},
+                      {w_scale_dev, weights * k_in / 32, false},
+                      {plan->cu_seqlens, (int64_t)dims->n_ranks * (g.NS + 1) * 4, false},
+                      {plan->rep_expert, (int64_t)dims->n_ranks * dims->slots_per_rank * 4, false},
+                      {plan->status, 16, false}}))
+    return MB_ERR_INVALID_ARG;
   return launch_expert_mx4(*dims, g, *plan, n_out, k_in, a_dev, a_scale_dev, w_dev, w_scale_dev,
                            y_dev, stream) == hipSuccess
              ? MB_OK
