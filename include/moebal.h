@@ -471,7 +471,8 @@ int mb_rmsnorm_fp8(int32_t n_rows, int32_t hidden, int32_t dtype, float eps, con
  * block has s = 0. A block holding a NaN or an infinity has s = 255 (NaN)
  * and zero elements.
  *  act         MB_ACT_NONE: v = x; MB_ACT_SWIGLU: x rows are [gate | up] of
- *              2*hidden elements and v = gate / (1 + exp(-gate)) * up in fp32.
+ *              2*hidden elements and v = gate / (1 + exp(-gate)) * up in fp32,
+ *              also where exp(-gate) passes binary32.
  *  x_dev       [n_rows, hidden or 2*hidden] of dtype (MB_F32, MB_BF16).
  *  row_src_dev [n_rows] int32 or NULL: rows with a negative entry (the
  *              padding rows of a plan's row_src) are not written.

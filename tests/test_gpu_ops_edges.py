@@ -141,3 +141,32 @@ def test_outputs_beside_their_inputs_and_over_them():
     with pytest.raises(ValueError, match="overlap"):
         p.run(over)
     p.check(p.run())
+
+
+# -------------------------------------------------------------- 4-bit rows
+
+@pytest.mark.parametrize("up", [1.0, 3e30])
+@pytest.mark.parametrize("lo,hi", [(-100.0, -88.7), (-88.7, -87.3), (-87.3, -80.0), (-30.0, -10.0), (10.0, 90.0)])
+def test_swiglu_blocks_of_far_gates(lo, hi, up):
+    """Whole blocks whose sigmoids are near or below the smallest normal
+    number. The activation in binary32, in units of 2^-24: two exponentials (2
+    each) and their corrections (1 each), a sum (1), a reciprocal (2) and four
+    products (1 each): 13, below 2^-20 relative, which moves a code only where
+    the value is that close to a midpoint."""
+    r = rng(abs(int(lo)), 3)
+    m, h = 33, 256
+    x = np.empty((m, 2 * h), np.float32)
+    x[:, :h] = r.uniform(lo, hi, (m, h))
+    x[:, h:] = up * r.uniform(0.5, 1.0, (m, h))
+    v = R.swiglu(x)
+    q = torch.full((m, h // 2), 0xA5, dtype=torch.uint8, device=G.dev())
+    s = torch.full((m, h // 32), 0xA5, dtype=torch.uint8, device=G.dev())
+    mb.quantize_mx4(dev(x), q, s, act="swiglu")
+    s = s.cpu().numpy()
+    near = R.mx4_scale_bytes(v * (1 - 2.0**-20)), R.mx4_scale_bytes(v * (1 + 2.0**-20))
+    assert ((s == near[0]) | (s == near[1])).all()
+    unit = np.repeat(2.0 ** (s.astype(np.float64) - 127), 32, axis=1)
+    a = np.abs(v) / unit
+    half = np.where(a < 2, 0.25, np.where(a < 4, 0.5, 1.0)) * unit
+    err = np.abs(R.mx4_values(q.cpu().numpy(), s) - np.clip(v, -6 * unit, 6 * unit))
+    assert np.all(err <= half + 2.0**-20 * np.abs(v)), (err / (half + 2.0**-20 * np.abs(v))).max()

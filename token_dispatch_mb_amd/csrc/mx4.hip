@@ -52,6 +52,31 @@ __device__ __forceinline__ void quantize_chunk(const float* v, size_t at, uint32
   if ((at & 3) == 0) q_scale[at >> 2] = (uint8_t)s;
 }
 
+// g / (1 + exp(-g)) * up for gates from kNearGate on: the exponential's
+// argument is off by |g| 2^-24 of rounding, so the whole by less than 2^-19.
+constexpr float kNearGate = -16.0f;
+
+__device__ __forceinline__ float swiglu_near(float g, float up) {
+  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * up;
+}
+
+// The same for any gate, by h = exp(-|g| / 2): g / (1 + h h) * up, and two
+// factors h more for a negative g, one on each side, so that nothing on the
+// way overflows or falls below the normal numbers before the result does (the
+// reciprocal of 1 + exp(-g) does from -87.3). What the exponential's argument
+// loses by its rounding and its constant's comes back as a factor: below 2^-20.
+// 65536 rows of 2 x 2048 bf16 by this alone take 116 us, by the near form 106.
+__device__ __forceinline__ float swiglu_any(float g, float up) {
+  constexpr float kHalfLog2e = 0x1.715476p-1f, kLn2 = 0x1.62e43p-1f;
+  constexpr float kRest = 0x1.cab1b6p-28f;  // log2(e) / 2 less its constant, times ln 2
+  const float m = -fabsf(g), t = m * kHalfLog2e;
+  const float rest = fmaf(m, kRest, fmaf(m, kHalfLog2e, -t) * kLn2);
+  float h = __builtin_amdgcn_exp2f(t);
+  h = fmaf(h, rest, h);
+  const float r = __builtin_amdgcn_rcpf(fmaf(h, h, 1.0f)), f = g < 0.0f ? h : 1.0f;
+  return g * f * r * (f * up);
+}
+
 // All rows of x, one after the other.
 template <bool kBF16>
 __global__ __launch_bounds__(kMxThreads) void k_quantize_mx4(const void* x, uint32_t* q,
@@ -65,7 +90,7 @@ __global__ __launch_bounds__(kMxThreads) void k_quantize_mx4(const void* x, uint
 
 // Row by row, for rows with an activation or that may be skipped: one wave
 // per 64 chunks of a row, a row's parts on consecutive waves. The activation
-// is not rounded before it is quantised. 65536 rows of 2 x 2048 bf16: 107 us,
+// is not rounded before it is quantised. 65536 rows of 2 x 2048 bf16: 106 us,
 // 5.7 TB/s.
 template <bool kBF16, bool kSwiglu>
 __global__ __launch_bounds__(kMxThreads) void k_quantize_mx4_rows(const void* x,
@@ -82,9 +107,16 @@ __global__ __launch_bounds__(kMxThreads) void k_quantize_mx4_rows(const void* x,
     load8<kBF16>(x, (size_t)row * 2 * chunks + c, v);
     load8<kBF16>(x, ((size_t)row * 2 + 1) * chunks + c, up);
     if (row_src && row_src[row] < 0) return;
+    float low = v[0];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      v[i] = v[i] * __builtin_amdgcn_rcpf(1.0f + __expf(-v[i])) * up[i];
+    for (int i = 1; i < 8; ++i) low = fminf(low, v[i]);
+    if (ballot64(low < kNearGate) == 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = swiglu_near(v[i], up[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = swiglu_any(v[i], up[i]);
+    }
   } else {
     load8<kBF16>(x, (size_t)row * chunks + c, v);
     if (row_src && row_src[row] < 0) return;
