@@ -10,6 +10,7 @@ namespace mb {
 namespace {
 
 constexpr int kNormThreads = 512;
+static_assert(MB_MAX_NORM_HIDDEN <= 4 * 8 * kNormThreads, "at most four chunks to a lane");
 constexpr float kE4m3Max = 448.0f;
 
 // One workgroup per row, a lane per 8 consecutive elements, the row in
@@ -101,10 +102,8 @@ void launch_norm_t(int n_rows, int hidden, float eps, const void* x, const void*
     MB_N(1);
   else if (cpt <= 2)
     MB_N(2);
-  else if (cpt <= 4)
-    MB_N(4);
   else
-    MB_N(8);
+    MB_N(4);
 #undef MB_N
 }
 
