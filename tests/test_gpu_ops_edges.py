@@ -10,7 +10,7 @@ import token_dispatch_mb_amd as mb
 
 from . import gpu_harness as G
 from . import plain_ops as R
-from .test_gpu_ops import Product, dev, rng
+from .test_gpu_ops import Product, check_norm, dev, rng
 
 pytestmark = pytest.mark.gpu
 
@@ -170,3 +170,17 @@ def test_swiglu_blocks_of_far_gates(lo, hi, up):
     half = np.where(a < 2, 0.25, np.where(a < 4, 0.5, 1.0)) * unit
     err = np.abs(R.mx4_values(q.cpu().numpy(), s) - np.clip(v, -6 * unit, 6 * unit))
     assert np.all(err <= half + 2.0**-20 * np.abs(v)), (err / (half + 2.0**-20 * np.abs(v))).max()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("eps", [0.0, 1e-42, 1e-30, 1e-20])
+def test_norm_of_rows_whose_squares_vanish(eps, dtype):
+    """Rows down to the smallest numbers: beside an epsilon as small, their
+    mean square is what counts, though binary32 does not hold it."""
+    r = rng(11)
+    x = r.standard_normal((12, 896)) * 10.0 ** -np.arange(14, 50, 3)[:, None]
+    x[3, 128:] = 0
+    w = 1 + 0.1 * r.standard_normal(896)
+    eps = float(np.float32(eps))  # as the call takes it: 1e-42 has 10 bits there
+    check_norm(x, w, eps, dtype)
+    check_norm(x, w, eps, dtype, residual=0.5 * x[::-1])

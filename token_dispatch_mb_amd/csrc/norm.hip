@@ -13,6 +13,23 @@ constexpr int kNormThreads = 512;
 static_assert(MB_MAX_NORM_HIDDEN <= 4 * 8 * kNormThreads, "at most four chunks to a lane");
 constexpr float kE4m3Max = 448.0f;
 
+// Mean squares (with epsilon) below kTinyMean, of which squares below the
+// normal numbers are a part that counts, are taken again from rows times
+// kLift: sums of at most 2^14 such squares stay below 2^114, and the smallest
+// number's square is 2^-98.
+constexpr float kTinyMean = 0x1p-100f, kLift = 0x1p100f;
+
+// Sum over the workgroup, the same in every lane.
+__device__ __forceinline__ float group_sum(float v, float* part) {
+  v = wave_sum_f32(v);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kNormThreads / 64; ++i) v += part[i];
+  return v;
+}
+
 // One workgroup per row, a lane per 8 consecutive elements, the row in
 // registers between its two passes (sum of squares; scales and codes), so
 // that memory is read and written once and bounds it. Squares are summed in
@@ -45,13 +62,24 @@ __global__ __launch_bounds__(kNormThreads) void k_rmsnorm_fp8(
       for (int j = 0; j < 8; ++j) ss = fmaf(h[i][j], h[i][j], ss);
     }
   }
-  ss = wave_sum_f32(ss);
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = ss;
-  __syncthreads();
-  ss = 0.0f;
+  ss = group_sum(ss, part);
+  float ms = ss / (float)(chunks * 8) + eps;
+  if (ms < kTinyMean) {  // the same for every lane
+    ss = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kNormThreads / 64; ++i) ss += part[i];
-  const float ms = ss / (float)(chunks * 8) + eps;
+    for (int i = 0; i < CPT; ++i) {
+      if (i * kNormThreads + (int)threadIdx.x < chunks) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          h[i][j] *= kLift;
+          ss = fmaf(h[i][j], h[i][j], ss);
+        }
+      }
+    }
+    __syncthreads();  // every lane has read the first sums
+    ss = group_sum(ss, part);
+    ms = ss / (float)(chunks * 8) + eps * kLift * kLift;
+  }
   float inv = ms > 0.0f ? 1.0f / sqrtf(ms) : 0.0f;
   const bool bad = !(ss < INFINITY);  // a NaN or an infinity in the row, or a sum past binary32
   if (bad) inv = NAN;
