@@ -184,3 +184,40 @@ def test_norm_of_rows_whose_squares_vanish(eps, dtype):
     eps = float(np.float32(eps))  # as the call takes it: 1e-42 has 10 bits there
     check_norm(x, w, eps, dtype)
     check_norm(x, w, eps, dtype, residual=0.5 * x[::-1])
+
+
+# ------------------------------------------------- the dispatch of 4-bit rows
+
+@pytest.mark.parametrize("shift", [0, 4])
+@pytest.mark.parametrize("h,k", [(128, 2), (896, 3), (4096, 1), (4096, 2), (4096, 16), (4096, 17),
+                                 (7168, 8), (7168, 4), (8192, 8), (8192, 5)])
+def test_dispatch_of_4_bit_rows(h, k, shift):
+    """Rows of any length, those of whole 2 KiB spans among them, with their
+    scales at 16-byte and at other addresses: every row and scale row of the
+    plan is its token's, the padding stays as it was."""
+    n, e, p = 136, 32, 4
+    r = rng(h, k)
+    ids = np.stack([r.permutation(e)[:k] for _ in range(n)]).astype(np.int32)
+    dims = mb.Dims.make(n, k, e, p, 2, h, cap=2 * n // p * k + 64, dtype_in="mx4")
+    plan = G.GpuPlan(dims)
+    plan.run(ids)
+    x = dev(r.integers(0, 256, (n, h // 2), dtype=np.uint8))
+    words = h // 32
+
+    def at(t):  # the same bytes, `shift` behind a 16-byte address
+        m = torch.full((t.numel() + shift,), 0xA5, dtype=torch.uint8, device=G.dev())
+        m[shift:] = t.reshape(-1)
+        return m[shift:].view(t.shape)
+
+    xs = at(dev(r.integers(0, 256, (n, words), dtype=np.uint8)))
+    buf = torch.full((dims.rows, h // 2), 0x5A, dtype=torch.uint8, device=G.dev())
+    bs = at(torch.full((dims.rows, words), 0x5A, dtype=torch.uint8, device=G.dev()))
+    mb.dispatch(dims, plan.bufs, x, buf, xs, bs)
+    torch.cuda.synchronize()
+    assert int(plan.bufs.status[0]) & mb.ST_FATAL == 0
+    src = plan.bufs.row_src.long().view(-1)
+    used = src >= 0
+    token = src[used]
+    assert len(token) == n * k
+    assert torch.equal(buf[used], x[token]) and torch.equal(bs[used], xs[token])
+    assert (buf[~used] == 0x5A).all() and (bs[~used] == 0x5A).all()
