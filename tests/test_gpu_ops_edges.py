@@ -186,6 +186,26 @@ def test_norm_of_rows_whose_squares_vanish(eps, dtype):
     check_norm(x, w, eps, dtype, residual=0.5 * x[::-1])
 
 
+def test_norm_of_more_rows_than_one_launch_holds():
+    """512 threads to a row, and fewer than 2^32 to a launch: from 2^23 - 2
+    rows on there are several, each with its own part of every tensor."""
+    n, h = (1 << 23) + 1001, 128
+    g = G.dev()
+    x = torch.empty(n, h, dtype=torch.bfloat16, device=g).normal_()
+    res = torch.empty_like(x).normal_()
+    w = torch.empty(h, dtype=torch.bfloat16, device=g).uniform_(0.5, 2)
+    q = torch.full((n, h), 0xA5, dtype=torch.uint8, device=g)
+    qs = torch.full((n, 1), -5.0, device=g)
+    y, out = torch.zeros_like(x), torch.zeros_like(x)
+    mb.rmsnorm_fp8(x, w, 1e-6, q, qs, residual=res, residual_out=out, y=y)
+    for at in (slice(0, 700), slice((1 << 23) - 400, (1 << 23) + 300), slice(n - 700, n)):
+        one = [t[at].clone() for t in (x, res)]
+        q1, qs1, y1, o1 = (torch.empty_like(t[at]) for t in (q, qs, y, out))
+        mb.rmsnorm_fp8(one[0], w, 1e-6, q1, qs1, residual=one[1], residual_out=o1, y=y1)
+        for a, b in ((q, q1), (qs, qs1), (y, y1), (out, o1)):
+            assert torch.equal(a[at], b)
+
+
 # ------------------------------------------------- the dispatch of 4-bit rows
 
 @pytest.mark.parametrize("shift", [0, 4])

@@ -122,17 +122,27 @@ void launch_norm_t(int n_rows, int hidden, float eps, const void* x, const void*
                    hipStream_t st) {
   const int chunks = hidden / 8;
   const int cpt = (chunks + kNormThreads - 1) / kNormThreads;
-  uint32_t* q4 = reinterpret_cast<uint32_t*>(q);
-#define MB_N(C)                                                                                  \
-  hipLaunchKernelGGL((k_rmsnorm_fp8<kBF16, C>), dim3(n_rows), dim3(kNormThreads), 0, st, x, res, \
-                     weight, res_out, y, q4, q_scale, chunks, eps)
-  if (cpt <= 1)
-    MB_N(1);
-  else if (cpt <= 2)
-    MB_N(2);
-  else
-    MB_N(4);
+  auto at = [&](const void* p, int row) {  // row `row` of p, null where there is none
+    return p ? static_cast<const char*>(p) + (size_t)row * hidden * (kBF16 ? 2 : 4) : nullptr;
+  };
+  // a launch holds fewer than 2^32 threads
+  constexpr int kMost = kMaxWaves / (kNormThreads / 64);
+  for (int row = 0; row < n_rows; row += kMost) {
+    const dim3 grid(min(n_rows - row, kMost));
+    uint32_t* q4 = reinterpret_cast<uint32_t*>(q + (size_t)row * hidden);
+#define MB_N(C)                                                                              \
+  hipLaunchKernelGGL((k_rmsnorm_fp8<kBF16, C>), grid, dim3(kNormThreads), 0, st, at(x, row), \
+                     at(res, row), weight, const_cast<char*>(at(res_out, row)),              \
+                     const_cast<char*>(at(y, row)), q4, q_scale + (size_t)row * (hidden / 128), \
+                     chunks, eps)
+    if (cpt <= 1)
+      MB_N(1);
+    else if (cpt <= 2)
+      MB_N(2);
+    else
+      MB_N(4);
 #undef MB_N
+  }
 }
 
 }  // namespace
