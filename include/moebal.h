@@ -411,7 +411,9 @@ typedef struct mb_route_params {
  * order (ties: the lowest id); w_k = score, divided by the sum of the K when
  * renorm is set, times scale. The choice is the one exact arithmetic on the
  * given logits and biases makes: values too close for binary32 are compared
- * in binary64. The weights are binary32.
+ * in binary64, and count as tied where that cannot tell them apart (two
+ * sigmoids that are both 1 to 53 bits). Without a bias, and with group scores
+ * of one expert, the logits themselves are compared. The weights are binary32.
  * Masks: an expert whose logit or bias is -inf or NaN is masked. Its choice
  * value is -inf, so it is taken only when fewer than K others are open (ids
  * ascending, always K distinct ids), and its weight is 0; the softmax sums
@@ -450,8 +452,7 @@ int mb_route(const mb_route_params* prm, const void* logits_dev, const float* bi
  *  residual_out_dev  [n_rows, H] h rounded to dtype (round to nearest even);
  *                    NULL to not store it. May be x_dev or residual_dev
  *                    themselves (in place); no other overlap is allowed
- *                    (refused).
- *                    Needs residual_dev.
+ *                    (refused). Needs residual_dev.
  *  y_dev             [n_rows, H] the normed rows in dtype, or NULL.
  *  q_dev             [n_rows, H] fp8 codes.
  *  q_scale_dev       [n_rows, H/128] fp32 scales.
@@ -486,7 +487,8 @@ int mb_quantize_mx4(int32_t n_rows, int32_t hidden, int32_t dtype, int32_t act, 
                     hipStream_t stream);
 
 /* The values of microscaled 4-bit rows, as rows of dtype (MB_F32 or MB_BF16;
- * both hold them exactly). A scale of 255 gives NaN. Layouts, limits and
+ * both hold them exactly, but for values of 2^128 and more under scales 253 and
+ * 254, which are infinite). A scale of 255 gives NaN. Layouts, limits and
  * alignment as mb_quantize_mx4; x overlaps no input (refused). */
 int mb_dequantize_mx4(int32_t n_rows, int32_t hidden, int32_t dtype, const uint8_t* q_dev,
                       const uint8_t* q_scale_dev, void* x_dev, hipStream_t stream);
@@ -498,16 +500,18 @@ int mb_dequantize_mx4(int32_t n_rows, int32_t hidden, int32_t dtype, const uint8
  * microscaled 4-bit rows and weights, accumulated in fp32, stored as
  * dims->dtype_out (bf16: round to nearest even). Rows no slot covers are not
  * written. An empty slot, or a replica slot holding no expert, costs nothing.
- *  n_out, k_in  outputs per row and their terms: k_in % 128 == 0, n_out rows
- *               a multiple of 16 bytes.
+ *  n_out, k_in  outputs per row and their terms, at most 2^20 each: k_in % 128
+ *               == 0, n_out rows a multiple of 16 bytes, and (P*cap/16 +
+ *               slots) * ceil(n_out/16) < 2^31.
  *  a_dev        [P*cap, k_in/2], a_scale_dev [P*cap, k_in/32].
  *  w_dev        [E, n_out, k_in/2], w_scale_dev [E, n_out, k_in/32].
  *  y_dev        [P*cap, n_out] of dtype_out.
  * Reads plan->cu_seqlens, rep_expert and status; does nothing under a fatal
  * status. dims gives E, P, R, cap, N*K (the rows expected, which picks the
- * tile size) and dtype_out; hidden and dtype_in are not used. P*cap is at most
- * 2^31 - 256 here (rows up to a whole tile behind the last one are numbered). a, w and y
- * 16-byte aligned, the scales 4-byte; y overlaps no input (refused).
+ * tile size) and dtype_out; hidden and dtype_in only have to be valid. P*cap
+ * is at most 2^31 - 256 here (rows up to a whole tile behind the last one are
+ * numbered). a, w and y 16-byte aligned, the scales 4-byte; y overlaps no input
+ * (refused).
  */
 int mb_expert_mx4(const mb_dims* dims, const mb_plan_bufs* plan, int32_t n_out, int32_t k_in,
                   const uint8_t* a_dev, const uint8_t* a_scale_dev, const uint8_t* w_dev,

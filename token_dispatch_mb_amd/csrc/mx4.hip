@@ -15,9 +15,10 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 // Both directions are bound by memory: a lane per 8 elements (16 bytes of
 // bf16, 4 of codes), four lanes per block of 32. Measured on MI355X for 8192 x
-// 7168 bf16 rows: 22 us to quantise, 21 us back (6.8 TB/s: the codes stay in
-// the last-level cache). With two or four chunks of a lane in flight both
-// together took 2 and 8 % longer (51, 54 against 50 us).
+// 7168 bf16 rows: 22-25 us to quantise, 21 us back, 47 in all (6.4 TB/s: the
+// codes stay in the last-level cache). With two or four chunks of a lane in
+// flight both together took 2 and 8 % longer (51, 54 against 50 us, all three
+// with plain stores).
 
 // Scale byte of a block from the bits of its largest magnitude: 127 +
 // floor(log2(amax)) - 2, at least 0, which is the bits' exponent less 2 for a

@@ -35,8 +35,8 @@ __device__ __forceinline__ float group_sum(float v, float* part) {
 // that memory is read and written once and bounds it. Squares are summed in
 // binary32; the normed value is rounded once, to e4m3 (and once more, from
 // the same binary32 value, to dtype in y). Measured on MI355X: 131072 x 7168
-// bf16 with the residual 1.14 ms, 5.8 TB/s of 6.6 GB; 4099 x 4224 fp32 27 us,
-// 5.7 TB/s; one row 2.8 us. 256 or 1024 lanes to a row were 2 and 4 % slower
+// bf16 with the residual 1.11-1.14 ms, 5.8-6.0 TB/s of 6.6 GB; 4099 x 4224 fp32 28
+// us, 5.5 TB/s; one row 3.0 us. 256 or 1024 lanes to a row were 2 and 4 % slower
 // on the first, 8 and 1 % on the second.
 template <bool kBF16, int CPT>
 __global__ __launch_bounds__(kNormThreads) void k_rmsnorm_fp8(

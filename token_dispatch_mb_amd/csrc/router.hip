@@ -1,8 +1,9 @@
 // router.hip — router logits to expert ids and gate weights (mb_route).
 //
-// The choice is exact: choice values are formed and compared in binary64,
-// so that it is the one the definition makes on the given logits and biases
-// (two values closer than binary64 resolves count as tied). Where the order
+// The choice is exact: choice values are formed and compared in binary64
+// wherever binary32 cannot tell them apart, so that it is the one the
+// definition makes on the given logits and biases (two values closer than
+// binary64 resolves count as tied). Where the order
 // of the choice values is the order of the logits (no bias, group scores
 // that are a maximum), the logits themselves are compared.
 #include <math.h>
@@ -16,7 +17,7 @@ namespace mb {
 namespace {
 
 constexpr int kRouteWaves = 4;
-constexpr int kRouteGroups = 2048;  // workgroups of one launch: eight on each CU
+constexpr int kRouteGroups = 2048;  // workgroups of one launch: eight for each CU, two to five of them at a time
 
 template <bool kBF16>
 __device__ __forceinline__ float load_logit(const void* p, size_t i) {
@@ -261,7 +262,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route(RouteArgs a) {
 // experts in 8 groups, fp32, sigmoid and bias: 64 us (2.2 TB/s; a wave per
 // token in binary64 takes 355); without route_exact's rows, a few in 100000,
 // it would be 13 us less, their one long chain being the tail. 65536 x 384,
-// softmax: 29 us (3.5 TB/s). 8192 x 256, bf16: 11 us.
+// softmax: 31 us (3.4 TB/s). 8192 x 256, bf16: 9 us, and 16 with a row redone.
 
 // By value: of two array elements the compiler would choose the index.
 __device__ __forceinline__ int choose(bool c, int a, int b) { return c ? a : b; }
@@ -584,7 +585,10 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_rows(RouteArgs a, in
   }
 }
 
-// Whether k_route_rows<V> takes these sizes: groups must be whole lanes.
+// Whether k_route_rows<V> takes these sizes: groups must be whole lanes, and
+// are found by a lane's place alone, so that the row must be full of them. (Other
+// sizes run in binary64, about five times slower: 131072 x 256 by k_route 355 us,
+// 64 here.)
 bool rows_fit(const RouteArgs& a, int V, bool grouped) {
   if (a.K > 14) return false;
   if (!grouped) return true;
@@ -599,6 +603,10 @@ bool launch_rows(const RouteArgs& a, hipStream_t st) {
   if (!rows_fit(a, V, grouped)) return false;
   const int quads = (a.N + 3) / 4;
   const dim3 grid(min((quads + kRouteWaves - 1) / kRouteWaves, kRouteGroups)), block(64 * kRouteWaves);
+  // K = 8, the K of this library's large workloads, has its rounds unrolled
+  // where scores are compared (131072 x 256: 69 us in a loop, 63 unrolled).
+  // Other K, and comparisons by logits (65536 x 384: 30.6 us in a loop, 29.2
+  // unrolled), share the loop: each K is six more kernels to a type.
 #define MB_R(L, G)                                                                               \
   do {                                                                                           \
     if (a.K == 8 && V >= 8 && !L)                                                                \

@@ -37,7 +37,7 @@ __device__ __forceinline__ void load8(const void* p, size_t c, float* v) {
 }
 
 // Nontemporal: rows leave for memory (8192 x 7168 bf16 rows read back from
-// 4 bits: 46 us with the quantisation before it, 51 with plain stores; the
+// 4 bits: 46-47 us with the quantisation before it, 50-51 with plain stores; the
 // norm of 131072 such rows 2 % faster).
 template <bool kBF16>
 __device__ __forceinline__ void store8(void* p, size_t c, const float* v) {
