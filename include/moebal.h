@@ -518,6 +518,71 @@ int mb_expert_mx4(const mb_dims* dims, const mb_plan_bufs* plan, int32_t n_out, 
                   const uint8_t* w_scale_dev, void* y_dev, hipStream_t stream);
 
 /*
+ * Experts' products over the dispatch layout from bf16 rows and weights: for
+ * every row p of every slot, e the expert the slot holds,
+ *   MB_ACT_NONE    y[p][j] = sum_i a[p][i] * w[e][j][i];
+ *   MB_ACT_SWIGLU  g and u are such sums with the weight rows j and n_out + j,
+ *                  y[p][j] = g / (1 + exp(-g)) * u: both projections of a gated
+ *                  feed-forward block and its activation,
+ * accumulated in fp32 and rounded once (to nearest even). Rows no slot covers
+ * are not written. An empty slot, or a replica slot holding no expert, costs
+ * nothing.
+ *  n_out, k_in  outputs per row and their terms: multiples of 8, at most 2^20
+ *               each, and (P*cap/16 + slots) * ceil(max(n_out, k_in)/16) and
+ *               E * ceil(n_out/128) * ceil(k_in/128) below 2^31.
+ *  a_dev        [P*cap, k_in] bf16.
+ *  w_dev        [E, n_out, k_in] bf16; MB_ACT_SWIGLU: [E, 2*n_out, k_in], the
+ *               gate's rows, then up's.
+ *  y_dev        [P*cap, n_out] of dtype_out; MB_ACT_SWIGLU: bf16.
+ *  pre_dev      MB_ACT_SWIGLU: [P*cap, 2*n_out] bf16, g and u of every row for
+ *               mb_expert_bf16_dgrad, or NULL to not store them; else NULL.
+ * Reads plan->cu_seqlens, rep_expert and status; does nothing under a fatal
+ * status. dims gives E, P, R, cap, N*K (the rows expected, which picks the
+ * kernel) and dtype_out; hidden and dtype_in only have to be valid. P*cap is
+ * at most 2^31 - 256. All pointers 16-byte aligned; outputs overlap neither each
+ * other nor an input (refused).
+ */
+int mb_expert_bf16(const mb_dims* dims, const mb_plan_bufs* plan, int32_t act, int32_t n_out,
+                   int32_t k_in, const uint16_t* a_dev, const uint16_t* w_dev, void* y_dev,
+                   uint16_t* pre_dev, hipStream_t stream);
+
+/*
+ * The gradient of a product's rows (n_out, k_in and w as in the product):
+ *   MB_ACT_NONE    da[p][i] = sum_j dy[p][j] * w[e][j][i];
+ *   MB_ACT_SWIGLU  the rows were silu(g) * u of pre = [g | u]: with d that sum
+ *                  and s = 1 / (1 + exp(-g)), da[p] = [dg | du],
+ *                  dg[i] = d * u * s * (1 + g * (1 - s)), du[i] = d * g * s.
+ *  dy_dev   [P*cap, n_out] bf16.
+ *  w_dev    [E, n_out, k_in] bf16.
+ *  pre_dev  MB_ACT_SWIGLU: [P*cap, 2*k_in] bf16, as mb_expert_bf16 stored it;
+ *           else NULL.
+ *  da_dev   [P*cap, k_in] of dtype_out; MB_ACT_SWIGLU: [P*cap, 2*k_in] bf16.
+ * A block y = (silu(g) * u) w2^T with [g | u] = x w1^T has the gradients
+ *   dpre = dgrad(SWIGLU, dy, w2, pre), dw2 = wgrad(dy, silu(g) * u),
+ *   dx = dgrad(NONE, dpre, w1), dw1 = wgrad(dpre, x).
+ * Everything else as mb_expert_bf16.
+ */
+int mb_expert_bf16_dgrad(const mb_dims* dims, const mb_plan_bufs* plan, int32_t act, int32_t n_out,
+                         int32_t k_in, const uint16_t* dy_dev, const uint16_t* w_dev,
+                         const uint16_t* pre_dev, void* da_dev, hipStream_t stream);
+
+/*
+ * The gradient of a product's weights:
+ *   dw[e][j][i] = sum_p dy[p][j] * a[p][i]
+ * over the rows p of every slot that holds e (its home slot, then its replica
+ * slots in ascending order: the same order, and result, every time),
+ * accumulated in fp32. An expert without rows gets zeros.
+ *  dtype       of dw: MB_F32 or MB_BF16 (round to nearest even).
+ *  accumulate  non-zero: the sum is added to what dw_dev holds.
+ *  dy_dev      [P*cap, n_out] bf16; a_dev [P*cap, k_in] bf16.
+ *  dw_dev      [E, n_out, k_in] of dtype.
+ * Everything else as mb_expert_bf16 (with N = 0 the plan is read all the same).
+ */
+int mb_expert_bf16_wgrad(const mb_dims* dims, const mb_plan_bufs* plan, int32_t n_out, int32_t k_in,
+                         int32_t dtype, int32_t accumulate, const uint16_t* dy_dev,
+                         const uint16_t* a_dev, void* dw_dev, hipStream_t stream);
+
+/*
  * Copy status[4] to host_status (host memory) after the work enqueued on
  * `stream` so far has finished. The only call that synchronises.
  */

@@ -164,11 +164,21 @@ _lib.mb_dequantize_mx4.restype = ctypes.c_int
 _lib.mb_expert_mx4.argtypes = [ctypes.POINTER(Dims), ctypes.POINTER(_PlanBufsC), _i32, _i32, _vp,
                                _vp, _vp, _vp, _vp, _vp]
 _lib.mb_expert_mx4.restype = ctypes.c_int
+_lib.mb_expert_bf16.argtypes = [ctypes.POINTER(Dims), ctypes.POINTER(_PlanBufsC), _i32, _i32, _i32,
+                                _vp, _vp, _vp, _vp, _vp]
+_lib.mb_expert_bf16.restype = ctypes.c_int
+_lib.mb_expert_bf16_dgrad.argtypes = [ctypes.POINTER(Dims), ctypes.POINTER(_PlanBufsC), _i32, _i32,
+                                      _i32, _vp, _vp, _vp, _vp, _vp]
+_lib.mb_expert_bf16_dgrad.restype = ctypes.c_int
+_lib.mb_expert_bf16_wgrad.argtypes = [ctypes.POINTER(Dims), ctypes.POINTER(_PlanBufsC), _i32, _i32,
+                                      _i32, _i32, _vp, _vp, _vp, _vp]
+_lib.mb_expert_bf16_wgrad.restype = ctypes.c_int
 
 EXPORTS = ("mb_version", "mb_strerror", "mb_plan_workspace_bytes", "mb_plan",
            "mb_plan_noalloc", "mb_plan_weighted", "mb_drift_state_bytes", "mb_plan_drift", "mb_plan_ex",
            "mb_dispatch", "mb_combine", "mb_combine_fp8", "mb_plan_status", "mb_route",
-           "mb_rmsnorm_fp8", "mb_quantize_mx4", "mb_dequantize_mx4", "mb_expert_mx4")
+           "mb_rmsnorm_fp8", "mb_quantize_mx4", "mb_dequantize_mx4", "mb_expert_mx4",
+           "mb_expert_bf16", "mb_expert_bf16_dgrad", "mb_expert_bf16_wgrad")
 ST_REPLANNED = 16
 ST_GUARDED = 32
 NOALLOC_WS_BYTES = 4 << 20
@@ -595,6 +605,82 @@ def expert_mx4(dims: Dims, bufs: PlanBuffers, n_out: int, k_in: int, a: torch.Te
                  (w_scale, wide * (k_in // 32), False), (y, rows * n_out * y.element_size(), True),
                  *((t, t.numel() * 4, False) for t in (bufs.cu_seqlens, bufs.rep_expert,
                                                        bufs.status)))
+
+
+def _plan_spans(bufs: PlanBuffers) -> tuple:
+    """The plan's arrays that the experts' products read, for `_refused`."""
+    return tuple((t, t.numel() * 4, False) for t in (bufs.cu_seqlens, bufs.rep_expert, bufs.status))
+
+
+def expert_bf16(dims: Dims, bufs: PlanBuffers, n_out: int, k_in: int, a: torch.Tensor,
+                w: torch.Tensor, y: torch.Tensor, act: str = "none",
+                pre: torch.Tensor | None = None, stream=None) -> None:
+    """mb_expert_bf16: y[p] = a[p] @ w[expert of p's slot].T over the plan's
+    rows, from bf16 rows a [P*cap, k_in] and weights [E, n_out, k_in]. With
+    act="swiglu" the weights are [E, 2 n_out, k_in] (gate rows, then up), y is
+    silu(gate) * up in bf16, and ``pre`` [P*cap, 2 n_out] keeps gate and up
+    for ``expert_bf16_dgrad``."""
+    rows, gated = dims.rows, ACTS[act] == ACT_SWIGLU
+    wide = dims.n_experts * n_out * (2 if gated else 1)
+    _check(a, "a", torch.bfloat16, numel=rows * k_in)
+    _check(w, "w", torch.bfloat16, numel=wide * k_in)
+    _check(y, "y", torch.bfloat16 if gated else TORCH_DTYPES.get(dims.dtype_out), numel=rows * n_out)
+    if pre is not None:
+        _check(pre, "pre", torch.bfloat16, numel=rows * 2 * n_out)
+    rc = _lib.mb_expert_bf16(ctypes.byref(dims), ctypes.byref(bufs.c_struct(dims)), ACTS[act], n_out,
+                             k_in, _ptr(a), _ptr(w), _ptr(y), _ptr(pre),
+                             _stream(stream, a, w, y, pre, bufs.status))
+    if rc != OK:
+        _refused("mb_expert_bf16", rc, (a, rows * k_in * 2, False), (w, wide * k_in * 2, False),
+                 (y, rows * n_out * y.element_size(), True), (pre, rows * n_out * 4, True),
+                 *_plan_spans(bufs))
+
+
+def expert_bf16_dgrad(dims: Dims, bufs: PlanBuffers, n_out: int, k_in: int, dy: torch.Tensor,
+                      w: torch.Tensor, da: torch.Tensor, act: str = "none",
+                      pre: torch.Tensor | None = None, stream=None) -> None:
+    """mb_expert_bf16_dgrad: the gradient of a product's rows, da[p] = dy[p] @
+    w[expert], from dy [P*cap, n_out] and the weights [E, n_out, k_in]. With
+    act="swiglu" the rows were silu(gate) * up of ``pre`` [P*cap, 2 k_in], and
+    da is the gradient of those, in bf16."""
+    rows, gated = dims.rows, ACTS[act] == ACT_SWIGLU
+    wide = k_in * (2 if gated else 1)
+    _check(dy, "dy", torch.bfloat16, numel=rows * n_out)
+    _check(w, "w", torch.bfloat16, numel=dims.n_experts * n_out * k_in)
+    _check(da, "da", torch.bfloat16 if gated else TORCH_DTYPES.get(dims.dtype_out),
+           numel=rows * wide)
+    if pre is not None:
+        _check(pre, "pre", torch.bfloat16, numel=rows * 2 * k_in)
+    rc = _lib.mb_expert_bf16_dgrad(ctypes.byref(dims), ctypes.byref(bufs.c_struct(dims)), ACTS[act],
+                                   n_out, k_in, _ptr(dy), _ptr(w), _ptr(pre), _ptr(da),
+                                   _stream(stream, dy, w, da, pre, bufs.status))
+    if rc != OK:
+        _refused("mb_expert_bf16_dgrad", rc, (dy, rows * n_out * 2, False),
+                 (w, dims.n_experts * n_out * k_in * 2, False),
+                 (da, rows * wide * da.element_size(), True), (pre, rows * k_in * 4, False),
+                 *_plan_spans(bufs))
+
+
+def expert_bf16_wgrad(dims: Dims, bufs: PlanBuffers, n_out: int, k_in: int, dy: torch.Tensor,
+                      a: torch.Tensor, dw: torch.Tensor, accumulate: bool = False,
+                      stream=None) -> None:
+    """mb_expert_bf16_wgrad: the gradient of a product's weights, dw[e] =
+    dy.T @ a over the rows of every slot that holds e, into dw [E, n_out, k_in]
+    (float32 or bfloat16); added to what dw holds with ``accumulate``."""
+    rows = dims.rows
+    _check(dy, "dy", torch.bfloat16, numel=rows * n_out)
+    _check(a, "a", torch.bfloat16, numel=rows * k_in)
+    _check(dw, "dw", numel=dims.n_experts * n_out * k_in)
+    if dw.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"dw must be torch.float32 or torch.bfloat16 (it is {dw.dtype})")
+    rc = _lib.mb_expert_bf16_wgrad(ctypes.byref(dims), ctypes.byref(bufs.c_struct(dims)), n_out, k_in,
+                                   F32 if dw.dtype == torch.float32 else BF16, int(bool(accumulate)),
+                                   _ptr(dy), _ptr(a), _ptr(dw),
+                                   _stream(stream, dy, a, dw, bufs.status))
+    if rc != OK:
+        _refused("mb_expert_bf16_wgrad", rc, (dy, rows * n_out * 2, False),
+                 (a, rows * k_in * 2, False),
+                 (dw, dims.n_experts * n_out * k_in * dw.element_size(), True), *_plan_spans(bufs))
 
 
 def plan_status(bufs: PlanBuffers, stream=None):

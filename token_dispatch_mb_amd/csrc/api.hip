@@ -476,6 +476,103 @@ int mb_expert_mx4(const mb_dims* dims, const mb_plan_bufs* plan, int32_t n_out, 
              : MB_ERR_HIP;
 }
 
+// What the products of bf16 rows share: the sizes, the plan and the region's
+// rows. `rows` and `weights`: rows of the dispatch layout, and of all experts.
+static bool bf16_product_ok(const mb_dims* dims, const mb_plan_bufs* plan, int32_t n_out,
+                            int32_t k_in, int64_t* rows, int64_t* weights) {
+  if (validate(dims) != MB_OK) return false;
+  if (n_out < 8 || n_out > kMaxExpertDim || n_out % 8) return false;
+  if (k_in < 8 || k_in > kMaxExpertDim || k_in % 8) return false;
+  if (!plan || !plan->status || !plan->cu_seqlens ||
+      (dims->slots_per_rank > 0 && !plan->rep_expert))
+    return false;
+  // a tile's rows are numbered in int32, also those behind the last region's end
+  if ((int64_t)dims->n_ranks * dims->cap > INT32_MAX - (kMaxTileRows - 1)) return false;
+  const Geometry g = geometry(*dims);
+  // output tiles of at least 16 rows x 16 columns, of the rows and of the
+  // weights, are numbered in int32
+  const int64_t row_tiles = (int64_t)dims->n_ranks * dims->cap / 16 + (int64_t)dims->n_ranks * g.NS;
+  const int64_t wide = ((n_out > k_in ? n_out : k_in) + 15) / 16;
+  if (row_tiles * wide > INT32_MAX) return false;
+  if ((int64_t)dims->n_experts * ((n_out + 127) / 128) * ((k_in + 127) / 128) > INT32_MAX)
+    return false;
+  *rows = dims->n_tokens ? (int64_t)dims->n_ranks * dims->cap : 0;
+  *weights = (int64_t)dims->n_experts * n_out;
+  return true;
+}
+
+// Nothing written overlaps the plan's arrays that the products read.
+static bool apart_from_plan(const mb_dims* dims, const mb_plan_bufs* plan, Span written) {
+  const Geometry g = geometry(*dims);
+  written.written = true;
+  return outputs_apart(
+      {written,
+       {plan->cu_seqlens, (int64_t)dims->n_ranks * (g.NS + 1) * 4, false},
+       {plan->rep_expert, (int64_t)dims->n_ranks * dims->slots_per_rank * 4, false},
+       {plan->status, 16, false}});
+}
+
+int mb_expert_bf16(const mb_dims* dims, const mb_plan_bufs* plan, int32_t act, int32_t n_out,
+                   int32_t k_in, const uint16_t* a_dev, const uint16_t* w_dev, void* y_dev,
+                   uint16_t* pre_dev, hipStream_t stream) {
+  int64_t rows, weights;
+  if (!bf16_product_ok(dims, plan, n_out, k_in, &rows, &weights)) return MB_ERR_INVALID_ARG;
+  if (act != MB_ACT_NONE && act != MB_ACT_SWIGLU) return MB_ERR_INVALID_ARG;
+  const bool gated = act == MB_ACT_SWIGLU;
+  if (!a_dev || !w_dev || !y_dev || (pre_dev && !gated)) return MB_ERR_INVALID_ARG;
+  if (!aligned16(a_dev) || !aligned16(w_dev) || !aligned16(y_dev) || !aligned16(pre_dev))
+    return MB_ERR_INVALID_ARG;
+  const Span y = {y_dev, rows * n_out * (gated ? 2 : elt_bytes(dims->dtype_out)), true};
+  const Span pre = {pre_dev, pre_dev ? rows * n_out * 4 : 0, true};
+  if (!outputs_apart({y, pre, {a_dev, rows * k_in * 2, false},
+                      {w_dev, weights * k_in * (gated ? 4 : 2), false}}) ||
+      !apart_from_plan(dims, plan, y) || !apart_from_plan(dims, plan, pre))
+    return MB_ERR_INVALID_ARG;
+  return launch_expert_bf16(*dims, geometry(*dims), *plan, gated, n_out, k_in, a_dev, w_dev, y_dev,
+                            pre_dev, stream) == hipSuccess
+             ? MB_OK
+             : MB_ERR_HIP;
+}
+
+int mb_expert_bf16_dgrad(const mb_dims* dims, const mb_plan_bufs* plan, int32_t act, int32_t n_out,
+                         int32_t k_in, const uint16_t* dy_dev, const uint16_t* w_dev,
+                         const uint16_t* pre_dev, void* da_dev, hipStream_t stream) {
+  int64_t rows, weights;
+  if (!bf16_product_ok(dims, plan, n_out, k_in, &rows, &weights)) return MB_ERR_INVALID_ARG;
+  if (act != MB_ACT_NONE && act != MB_ACT_SWIGLU) return MB_ERR_INVALID_ARG;
+  const bool gated = act == MB_ACT_SWIGLU;
+  if (!dy_dev || !w_dev || !da_dev || (pre_dev != nullptr) != gated) return MB_ERR_INVALID_ARG;
+  if (!aligned16(dy_dev) || !aligned16(w_dev) || !aligned16(da_dev) || !aligned16(pre_dev))
+    return MB_ERR_INVALID_ARG;
+  const Span da = {da_dev, rows * k_in * (gated ? 4 : elt_bytes(dims->dtype_out)), true};
+  if (!outputs_apart({da, {dy_dev, rows * n_out * 2, false}, {w_dev, weights * k_in * 2, false},
+                      {pre_dev, pre_dev ? rows * k_in * 4 : 0, false}}) ||
+      !apart_from_plan(dims, plan, da))
+    return MB_ERR_INVALID_ARG;
+  return launch_expert_bf16_dgrad(*dims, geometry(*dims), *plan, gated, n_out, k_in, dy_dev, w_dev,
+                                  pre_dev, da_dev, stream) == hipSuccess
+             ? MB_OK
+             : MB_ERR_HIP;
+}
+
+int mb_expert_bf16_wgrad(const mb_dims* dims, const mb_plan_bufs* plan, int32_t n_out, int32_t k_in,
+                         int32_t dtype, int32_t accumulate, const uint16_t* dy_dev,
+                         const uint16_t* a_dev, void* dw_dev, hipStream_t stream) {
+  int64_t rows, weights;
+  if (!bf16_product_ok(dims, plan, n_out, k_in, &rows, &weights)) return MB_ERR_INVALID_ARG;
+  if (dtype != MB_F32 && dtype != MB_BF16) return MB_ERR_INVALID_ARG;
+  if (!dw_dev || (dims->n_tokens > 0 && (!dy_dev || !a_dev))) return MB_ERR_INVALID_ARG;
+  if (!aligned16(dy_dev) || !aligned16(a_dev) || !aligned16(dw_dev)) return MB_ERR_INVALID_ARG;
+  const Span dw = {dw_dev, weights * k_in * elt_bytes(dtype), true};
+  if (!outputs_apart({dw, {dy_dev, rows * n_out * 2, false}, {a_dev, rows * k_in * 2, false}}) ||
+      !apart_from_plan(dims, plan, dw))
+    return MB_ERR_INVALID_ARG;
+  return launch_expert_bf16_wgrad(*dims, geometry(*dims), *plan, n_out, k_in, accumulate != 0,
+                                  dtype == MB_BF16, dy_dev, a_dev, dw_dev, stream) == hipSuccess
+             ? MB_OK
+             : MB_ERR_HIP;
+}
+
 int mb_plan_status(const mb_plan_bufs* plan, hipStream_t stream, int32_t host_status[4]) {
   if (!plan || !plan->status || !host_status) return MB_ERR_INVALID_ARG;
   if (hipMemcpyAsync(host_status, plan->status, 4 * sizeof(int32_t), hipMemcpyDeviceToHost,

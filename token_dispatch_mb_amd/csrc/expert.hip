@@ -11,18 +11,12 @@
 
 #include "mb_internal.h"
 #include "rowio.h"
-#include "wave.h"
+#include "slots.h"
 
 namespace mb {
 namespace {
 
-typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
-constexpr int kExpertThreads = 256;
-constexpr int kMaxPlanSlots = kMaxExperts + kMaxRanks * kMaxSlots;
 
 struct ExpertArgs {
   const uint8_t* a;
@@ -42,69 +36,12 @@ __device__ __forceinline__ f32x4 mfma_mx4(i32x4 a, i32x4 b, f32x4 c, int sa, int
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, 0, sa, 0, sb);
 }
 
-typedef const __attribute__((address_space(4))) int32_t* plan_ptr;
-
 // u: which byte of the lanes' scales (the builtin takes it as a constant).
 __device__ __forceinline__ f32x16 mfma_mx4(i32x4 a, i32x4 b, f32x16 c, int sa, int sb, int u) {
   const i32x8 a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0};
   const i32x8 b8 = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
   return u ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, 1, sa, 1, sb)
            : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, 0, sa, 0, sb);
-}
-
-// Rows [lo, hi) of slot j (r = j / NS), absolute in the buffer, and its
-// expert; empty when it holds none. Only a broken plan needs the clamps.
-__device__ __forceinline__ void slot_rows(const ExpertArgs& p, int j, int& lo, int& hi, int& e) {
-  const int r = j / p.NS, i = j - r * p.NS;
-  // the plan does not change under the kernel: constant memory
-  auto cu = (plan_ptr)(p.cu + (size_t)r * (p.NS + 1) + i);
-  lo = min(max(cu[0], 0), p.cap);
-  hi = min(max(cu[1], lo), p.cap);
-  e = i < p.Eh ? r * p.Eh + i : ((plan_ptr)p.rep)[(size_t)r * p.R + i - p.Eh];
-  if ((unsigned)e >= (unsigned)p.E) hi = lo;
-  lo += r * p.cap;
-  hi += r * p.cap;
-}
-
-// first[j] = row tiles of the slots before j, first[nslots] = all of them.
-template <int BM>
-__device__ void tile_table(const ExpertArgs& p, int nslots, int* first, int* part) {
-  const int per = (nslots + kExpertThreads - 1) / kExpertThreads;
-  const int j0 = threadIdx.x * per;
-  int sum = 0;
-  for (int j = j0; j < min(j0 + per, nslots); ++j) {
-    int lo, hi, e;
-    slot_rows(p, j, lo, hi, e);
-    sum += (hi - lo + BM - 1) / BM;
-  }
-  const int incl = wave_inclusive_sum(sum);
-  if ((threadIdx.x & 63) == 63) part[threadIdx.x >> 6] = incl;
-  __syncthreads();
-  int base = incl - sum;
-  for (int i = 0; i < (int)(threadIdx.x >> 6); ++i) base += part[i];
-  for (int j = j0; j < min(j0 + per, nslots); ++j) {
-    int lo, hi, e;
-    slot_rows(p, j, lo, hi, e);
-    first[j] = base;
-    base += (hi - lo + BM - 1) / BM;
-  }
-  if (threadIdx.x == kExpertThreads - 1) first[nslots] = base;
-  __syncthreads();
-}
-
-// The slot whose tiles hold row tile t.
-__device__ __forceinline__ int slot_of(const int* first, int nslots, int t) {
-  int lo = 0, hi = nslots;  // first[lo] <= t < first[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (first[mid] <= t) lo = mid;
-    else hi = mid;
-  }
-  return __builtin_amdgcn_readfirstlane(lo);
-}
-
-__device__ __forceinline__ i32x4 load16(const uint8_t* p) {
-  return *static_cast<const i32x4*>(__builtin_assume_aligned(p, 16));
 }
 
 // The scales of four steps; rows of scales are whole words.
@@ -124,11 +61,6 @@ __device__ __forceinline__ void store4(void* y, size_t at, f32x4 v) {
   }
 }
 
-// Waits until this wave's LDS reads are done, then for the other waves.
-__device__ __forceinline__ void read_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
 // Outputs [at, at + 8) of a row, as many as are left (a multiple of 4).
 template <bool kBF16>
 __device__ __forceinline__ void store8_of(void* y, size_t at, int left, f32x4 v, f32x4 u) {
@@ -141,14 +73,6 @@ __device__ __forceinline__ void store8_of(void* y, size_t at, int left, f32x4 v,
     if (left >= 4) store4<false>(y, at, v);
     if (left >= 8) store4<false>(y, at + 4, u);
   }
-}
-
-// Waits until this wave's LDS reads are done and at most N of its memory
-// operations (copies to LDS, stores) are outstanding, oldest first, then for
-// the other waves.
-template <int N>
-__device__ __forceinline__ void wait_barrier() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
 // ---- tiles staged through LDS -----------------------------------------------
@@ -186,33 +110,8 @@ __device__ __forceinline__ void wait_barrier() {
 // With random operands the card's power sets the clock (1.7 GHz; the products
 // alone, in a loop, reach 6.3 PFLOP/s, and 10 on zeros), so the parts add up
 // though they overlap. Accumulators of 16 x 16 x 128 took 8.4 ms here.
-constexpr int kTileN = 256;
-constexpr int kCus = 256, kXcds = 8;
 constexpr int kFewGroups = 2048;
-constexpr int kGroupM = 4;  // row tiles whose columns are walked together
 
-typedef __attribute__((address_space(3))) void* lds_ptr;
-
-// Buffer descriptor of `bytes` bytes at p (wave-uniform). A read at voff +
-// soff gives 0 where voff >= bytes - soff: soff must be below bytes, so what
-// may pass the end is always in voff.
-__device__ __forceinline__ i32x4 buffer_of(const void* p, uint32_t bytes) {
-  const uint64_t at = reinterpret_cast<uint64_t>(p);
-  return i32x4{__builtin_amdgcn_readfirstlane((int)at),
-               __builtin_amdgcn_readfirstlane((int)(at >> 32) & 0xffff),
-               __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
-}
-
-// Copies 64 lanes' 16 bytes at buf[voff + soff] to consecutive places of LDS
-// from `to` (wave-uniform; the instruction takes it from m0, one instruction
-// after m0 was written). No register is written. In assembly because the
-// compiler, for its builtin, waits for every copy in flight before the next
-// read of any LDS; the waits that order copies and reads are wait_barrier's.
-__device__ __forceinline__ void copy16(i32x4 buf, lds_ptr to, uint32_t voff, uint32_t soff) {
-  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-               ::"{m0}"((uint32_t)(uintptr_t)to), "v"(voff), "s"(buf), "s"(soff)
-               : "memory");
-}
 struct Tile {
   int m0, hi, n0, e;
 };

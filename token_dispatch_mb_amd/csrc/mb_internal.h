@@ -137,6 +137,17 @@ hipError_t launch_expert_mx4(const mb_dims& d, const Geometry& g, const mb_plan_
                              int32_t n_out, int32_t k_in, const uint8_t* a,
                              const uint8_t* a_scale, const uint8_t* w, const uint8_t* w_scale,
                              void* y, hipStream_t st);
+hipError_t launch_expert_bf16(const mb_dims& d, const Geometry& g, const mb_plan_bufs& o,
+                              bool gated, int32_t n_out, int32_t k_in, const uint16_t* a,
+                              const uint16_t* w, void* y, uint16_t* pre, hipStream_t st);
+hipError_t launch_expert_bf16_dgrad(const mb_dims& d, const Geometry& g, const mb_plan_bufs& o,
+                                    bool gated, int32_t n_out, int32_t k_in, const uint16_t* dy,
+                                    const uint16_t* w, const uint16_t* pre, void* da,
+                                    hipStream_t st);
+hipError_t launch_expert_bf16_wgrad(const mb_dims& d, const Geometry& g, const mb_plan_bufs& o,
+                                    int32_t n_out, int32_t k_in, bool add, bool bf16,
+                                    const uint16_t* dy, const uint16_t* a, void* dw,
+                                    hipStream_t st);
 
 // Launch KERNEL<K> for the top-K values with a specialised kernel, KERNEL<0>
 // (runtime K) otherwise.
