@@ -17,7 +17,10 @@
  * Around them: mb_route makes the ids and weights from the router's logits,
  * mb_rmsnorm_fp8 and mb_quantize_mx4 the 8- and 4-bit rows to dispatch, and
  * mb_expert_mx4 multiplies the dispatched 4-bit rows by their experts'
- * weights.
+ * weights. mb_expert_bf16 does so from bf16 rows and weights, as the two halves
+ * of a gated feed-forward block; its gradients and the combine's train such a
+ * layer. mb_project_lora serves the projections around the experts with the
+ * low-rank adapters of many requests.
  *
  * The P logical ranks of the expert-parallel group are partitions of one
  * GPU's memory: rank r owns rows [r*cap, (r+1)*cap) of every [P*cap, ...]
@@ -581,6 +584,72 @@ int mb_expert_bf16_dgrad(const mb_dims* dims, const mb_plan_bufs* plan, int32_t 
 int mb_expert_bf16_wgrad(const mb_dims* dims, const mb_plan_bufs* plan, int32_t n_out, int32_t k_in,
                          int32_t dtype, int32_t accumulate, const uint16_t* dy_dev,
                          const uint16_t* a_dev, void* dw_dev, hipStream_t stream);
+
+/*
+ * The gradients of mb_combine: for every pair (t, k), p = pos[t][k],
+ *   dy_exp[p][i] = w[t][k] * dy[t][i],
+ *   dw[t][k] = sum_i dy[t][i] * y_exp[p][i],
+ * in fp32, the rows rounded to dtype_out (to nearest even). (mb_dispatch's
+ * gradient is mb_combine with weights of 1.)
+ *  dy_dev      [N, H] of dtype_out.
+ *  y_exp_dev   [P*cap, H] of dtype_out, what the combine read; not read, and may
+ *              be NULL, without dw_dev.
+ *  w_dev       [N*K] fp32; not read, and may be NULL, without dy_exp_dev.
+ *  dy_exp_dev  [P*cap, H] of dtype_out, or NULL: not wanted. Padding rows are
+ *              not written.
+ *  dw_dev      [N*K] fp32, or NULL: not wanted (but one of the two is).
+ * Reads plan->pos and plan->status; does nothing under a fatal status. Rows
+ * 16-byte aligned, w and dw 4-byte; outputs overlap neither each other nor an
+ * input (refused).
+ */
+int mb_combine_grad(const mb_dims* dims, const mb_plan_bufs* plan, const void* dy_dev,
+                    const void* y_exp_dev, const float* w_dev, void* dy_exp_dev, float* dw_dev,
+                    hipStream_t stream);
+
+/* Largest rank of mb_project_lora. */
+#define MB_MAX_LORA_RANK 256
+
+/* Sizes of one projection with adapters. */
+typedef struct mb_lora_params {
+  int32_t n_rows;     /* rows (tokens) of all requests, in [0, 2^26] */
+  int32_t n_out;      /* outputs per row and their terms: multiples of 8, at most */
+  int32_t k_in;       /*   2^20; ceil(n_rows/16) * ceil(n_out/16) below 2^31 */
+  int32_t rank;       /* of every adapter (smaller ones padded with zeros): a
+                         multiple of 8 in [8, MB_MAX_LORA_RANK] */
+  int32_t n_adapters; /* L in [1, 2^20] */
+  int32_t dtype_out;  /* y: MB_F32 or MB_BF16 */
+} mb_lora_params;
+
+/* Bytes of device workspace mb_project_lora needs for these sizes; 0 for
+ * sizes outside the limits. Pure host function. */
+size_t mb_lora_workspace_bytes(const mb_lora_params* prm);
+
+/*
+ * A projection that all requests share, and beside it the low-rank adapter of
+ * each request (the projections around the experts: attention's, the shared
+ * expert's), a = adapter[t]:
+ *   y[t][j] = sum_i x[t][i] * w[j][i]
+ *           + sum_q (scale[a] * sum_i x[t][i] * lora_a[a][q][i]) * lora_b[a][j][q],
+ * the second line only where a is in [0, L): rows with any other number have no
+ * adapter. Accumulated in fp32 and rounded once (to nearest even); the inner
+ * sums are carried in 16 bits of mantissa. Rows of one adapter need not be
+ * consecutive, though a run of them costs less.
+ *  x_dev        [n_rows, k_in] bf16.
+ *  w_dev        [n_out, k_in] bf16.
+ *  lora_a_dev   [L, rank, k_in] bf16; lora_b_dev [L, n_out, rank] bf16.
+ *  scale_dev    [L] fp32.
+ *  adapter_dev  [n_rows] int32.
+ *  ws_dev       mb_lora_workspace_bytes(prm) bytes, 16-byte aligned; scratch. Calls
+ *               (and captured graphs) that may run at once need one each.
+ *  y_dev        [n_rows, n_out] of dtype_out.
+ * prm is host memory, read during the call only. Rows 16-byte aligned, scale
+ * and adapter 4-byte; y and ws overlap neither each other nor an input
+ * (refused). A workspace that is too small gives MB_ERR_WORKSPACE.
+ */
+int mb_project_lora(const mb_lora_params* prm, const uint16_t* x_dev, const uint16_t* w_dev,
+                    const uint16_t* lora_a_dev, const uint16_t* lora_b_dev,
+                    const float* scale_dev, const int32_t* adapter_dev, void* ws_dev,
+                    size_t ws_bytes, void* y_dev, hipStream_t stream);
 
 /*
  * Copy status[4] to host_status (host memory) after the work enqueued on

@@ -134,7 +134,7 @@ SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
 ACT_NONE, ACT_SWIGLU = 0, 1
 ACTS = {"none": ACT_NONE, "swiglu": ACT_SWIGLU}
-MAX_GROUPS, MAX_NORM_HIDDEN = 64, 16384
+MAX_GROUPS, MAX_NORM_HIDDEN, MAX_LORA_RANK = 64, 16384, 256
 
 
 class RouteParams(ctypes.Structure):
@@ -164,6 +164,28 @@ _lib.mb_dequantize_mx4.restype = ctypes.c_int
 _lib.mb_expert_mx4.argtypes = [ctypes.POINTER(Dims), ctypes.POINTER(_PlanBufsC), _i32, _i32, _vp,
                                _vp, _vp, _vp, _vp, _vp]
 _lib.mb_expert_mx4.restype = ctypes.c_int
+
+
+class LoraParams(ctypes.Structure):
+    """mb_lora_params."""
+
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "n_rows", "n_out", "k_in", "rank", "n_adapters", "dtype_out")]
+
+    @classmethod
+    def make(cls, n_rows, n_out, k_in, rank, n_adapters, dtype_out="bf16") -> "LoraParams":
+        return cls(n_rows, n_out, k_in, rank, n_adapters,
+                   DTYPES[dtype_out] if isinstance(dtype_out, str) else dtype_out)
+
+
+_lib.mb_combine_grad.argtypes = [ctypes.POINTER(Dims), ctypes.POINTER(_PlanBufsC), _vp, _vp, _vp,
+                                 _vp, _vp, _vp]
+_lib.mb_combine_grad.restype = ctypes.c_int
+_lib.mb_lora_workspace_bytes.argtypes = [ctypes.POINTER(LoraParams)]
+_lib.mb_lora_workspace_bytes.restype = ctypes.c_size_t
+_lib.mb_project_lora.argtypes = [ctypes.POINTER(LoraParams), _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                 ctypes.c_size_t, _vp, _vp]
+_lib.mb_project_lora.restype = ctypes.c_int
 _lib.mb_expert_bf16.argtypes = [ctypes.POINTER(Dims), ctypes.POINTER(_PlanBufsC), _i32, _i32, _i32,
                                 _vp, _vp, _vp, _vp, _vp]
 _lib.mb_expert_bf16.restype = ctypes.c_int
@@ -178,7 +200,8 @@ EXPORTS = ("mb_version", "mb_strerror", "mb_plan_workspace_bytes", "mb_plan",
            "mb_plan_noalloc", "mb_plan_weighted", "mb_drift_state_bytes", "mb_plan_drift", "mb_plan_ex",
            "mb_dispatch", "mb_combine", "mb_combine_fp8", "mb_plan_status", "mb_route",
            "mb_rmsnorm_fp8", "mb_quantize_mx4", "mb_dequantize_mx4", "mb_expert_mx4",
-           "mb_expert_bf16", "mb_expert_bf16_dgrad", "mb_expert_bf16_wgrad")
+           "mb_expert_bf16", "mb_expert_bf16_dgrad", "mb_expert_bf16_wgrad", "mb_combine_grad",
+           "mb_lora_workspace_bytes", "mb_project_lora")
 ST_REPLANNED = 16
 ST_GUARDED = 32
 NOALLOC_WS_BYTES = 4 << 20
@@ -681,6 +704,71 @@ def expert_bf16_wgrad(dims: Dims, bufs: PlanBuffers, n_out: int, k_in: int, dy: 
         _refused("mb_expert_bf16_wgrad", rc, (dy, rows * n_out * 2, False),
                  (a, rows * k_in * 2, False),
                  (dw, dims.n_experts * n_out * k_in * dw.element_size(), True), *_plan_spans(bufs))
+
+
+def combine_grad(dims: Dims, bufs: PlanBuffers, dy: torch.Tensor, y_exp: torch.Tensor | None,
+                 w: torch.Tensor | None, dy_exp: torch.Tensor | None,
+                 dw: torch.Tensor | None = None, stream=None) -> None:
+    """mb_combine_grad: the gradients of ``combine``, dy_exp[pos[t][k]] =
+    w[t][k] * dy[t] and dw[t][k] = dy[t] . y_exp[pos[t][k]]. Either output may
+    be None; y_exp is needed for dw only, w for dy_exp only."""
+    row, pairs = dims.hidden * ELT_BYTES.get(dims.dtype_out, 0), dims.n_tokens * dims.top_k
+    _check(dy, "dy", TORCH_DTYPES.get(dims.dtype_out), nbytes=dims.n_tokens * row)
+    if dw is not None:
+        _check(y_exp, "y_exp", dy.dtype, nbytes=dims.rows * row)
+        _check(dw, "dw", torch.float32, numel=pairs)
+    if dy_exp is not None:
+        _check(w, "w", torch.float32, numel=pairs)
+        _check(dy_exp, "dy_exp", dy.dtype, nbytes=dims.rows * row)
+    for name, t in (("y_exp", y_exp), ("w", w)):
+        if t is not None:
+            _check(t, name)
+    rc = _lib.mb_combine_grad(ctypes.byref(dims), ctypes.byref(bufs.c_struct(dims)), _ptr(dy),
+                              _ptr(y_exp), _ptr(w), _ptr(dy_exp), _ptr(dw),
+                              _stream(stream, dy, y_exp, w, dy_exp, dw, bufs.status))
+    if rc != OK:
+        _refused("mb_combine_grad", rc, (dy, dims.n_tokens * row, False),
+                 (y_exp if dw is not None else None, dims.rows * row, False),
+                 (w if dy_exp is not None else None, 4 * pairs, False),
+                 (dy_exp, dims.rows * row, True), (dw, 4 * pairs, True),
+                 (bufs.pos, 4 * pairs, False), (bufs.status, 16, False))
+
+
+def lora_workspace_bytes(prm: LoraParams) -> int:
+    return int(_lib.mb_lora_workspace_bytes(ctypes.byref(prm)))
+
+
+def alloc_lora_workspace(prm: LoraParams, device) -> torch.Tensor:
+    n = lora_workspace_bytes(prm)
+    if n == 0:
+        raise MoebalError("mb_lora_workspace_bytes", ERR_INVALID_ARG)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def project_lora(prm: LoraParams, x: torch.Tensor, w: torch.Tensor, lora_a: torch.Tensor,
+                 lora_b: torch.Tensor, scale: torch.Tensor, adapter: torch.Tensor,
+                 ws: torch.Tensor, y: torch.Tensor, stream=None) -> None:
+    """mb_project_lora: y[t] = x[t] @ w.T, plus scale[a] * (x[t] @ lora_a[a].T)
+    @ lora_b[a].T where a = adapter[t] is in [0, L); x [T, k_in], w [n_out,
+    k_in], lora_a [L, rank, k_in], lora_b [L, n_out, rank] in bf16, scale [L]
+    fp32, adapter [T] int32, ws from ``alloc_lora_workspace``."""
+    t, n, k, low = prm.n_rows, prm.n_out, prm.k_in, prm.n_adapters * prm.rank
+    _check(x, "x", torch.bfloat16, numel=t * k)
+    _check(w, "w", torch.bfloat16, numel=n * k)
+    _check(lora_a, "lora_a", torch.bfloat16, numel=low * k)
+    _check(lora_b, "lora_b", torch.bfloat16, numel=low * n)
+    _check(scale, "scale", torch.float32, numel=prm.n_adapters)
+    _check(adapter, "adapter", torch.int32, numel=t)
+    _check(ws, "ws")
+    _check(y, "y", TORCH_DTYPES.get(prm.dtype_out), numel=t * n)
+    rc = _lib.mb_project_lora(ctypes.byref(prm), _ptr(x), _ptr(w), _ptr(lora_a), _ptr(lora_b),
+                              _ptr(scale), _ptr(adapter), _ptr(ws), _nbytes(ws), _ptr(y),
+                              _stream(stream, x, w, lora_a, lora_b, scale, adapter, ws, y))
+    if rc != OK:
+        _refused("mb_project_lora", rc, (x, t * k * 2, False), (w, n * k * 2, False),
+                 (lora_a, low * k * 2, False), (lora_b, low * n * 2, False),
+                 (scale, 4 * prm.n_adapters, False), (adapter, 4 * t, False),
+                 (ws, lora_workspace_bytes(prm), True), (y, t * n * y.element_size(), True))
 
 
 def plan_status(bufs: PlanBuffers, stream=None):

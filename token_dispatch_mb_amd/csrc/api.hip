@@ -573,6 +573,81 @@ int mb_expert_bf16_wgrad(const mb_dims* dims, const mb_plan_bufs* plan, int32_t 
              : MB_ERR_HIP;
 }
 
+int mb_combine_grad(const mb_dims* dims, const mb_plan_bufs* plan, const void* dy_dev,
+                    const void* y_exp_dev, const float* w_dev, void* dy_exp_dev, float* dw_dev,
+                    hipStream_t stream) {
+  const int rc = validate(dims);
+  if (rc != MB_OK) return rc;
+  if (!plan || !plan->status || (!dy_exp_dev && !dw_dev)) return MB_ERR_INVALID_ARG;
+  if (dims->n_tokens > 0 && (!plan->pos || !dy_dev || (dw_dev && !y_exp_dev) ||
+                             (dy_exp_dev && !w_dev)))
+    return MB_ERR_INVALID_ARG;
+  if (!aligned16(dy_dev) || !aligned16(y_exp_dev) || !aligned16(dy_exp_dev) || !aligned4(w_dev) ||
+      !aligned4(dw_dev))
+    return MB_ERR_INVALID_ARG;
+  const int64_t row = dims->hidden * elt_bytes(dims->dtype_out), pairs = (int64_t)dims->n_tokens * dims->top_k;
+  const int64_t rows = dims->n_tokens ? (int64_t)dims->n_ranks * dims->cap : 0;
+  if (!outputs_apart({{dy_exp_dev, dy_exp_dev ? rows * row : 0, true},
+                      {dw_dev, dw_dev ? pairs * 4 : 0, true},
+                      {dy_dev, dims->n_tokens * row, false},
+                      {y_exp_dev, dw_dev ? rows * row : 0, false},
+                      {w_dev, dy_exp_dev ? pairs * 4 : 0, false},
+                      {plan->pos, pairs * 4, false},
+                      {plan->status, 16, false}}))
+    return MB_ERR_INVALID_ARG;
+  return launch_combine_grad(*dims, *plan, dy_dev, y_exp_dev, w_dev, dy_exp_dev, dw_dev, stream) ==
+                 hipSuccess
+             ? MB_OK
+             : MB_ERR_HIP;
+}
+
+static bool lora_ok(const mb_lora_params* p) {
+  if (!p || p->n_rows < 0 || p->n_rows > kMaxLoraRows) return false;
+  if (p->n_out < 8 || p->n_out > kMaxExpertDim || p->n_out % 8) return false;
+  if (p->k_in < 8 || p->k_in > kMaxExpertDim || p->k_in % 8) return false;
+  if (p->rank < 8 || p->rank > MB_MAX_LORA_RANK || p->rank % 8) return false;
+  if (p->n_adapters < 1 || p->n_adapters > kMaxAdapters) return false;
+  if (p->dtype_out != MB_F32 && p->dtype_out != MB_BF16) return false;
+  // output tiles of at least 16 x 16 are numbered in int32
+  return ((int64_t)p->n_rows + 15) / 16 * ((p->n_out + 15) / 16) <= INT32_MAX;
+}
+
+size_t mb_lora_workspace_bytes(const mb_lora_params* prm) {
+  if (!lora_ok(prm)) return 0;
+  const size_t v = (size_t)lora_parts(*prm) * prm->n_rows * prm->rank * sizeof(float);
+  return align256(v ? v : 1);
+}
+
+int mb_project_lora(const mb_lora_params* prm, const uint16_t* x_dev, const uint16_t* w_dev,
+                    const uint16_t* lora_a_dev, const uint16_t* lora_b_dev,
+                    const float* scale_dev, const int32_t* adapter_dev, void* ws_dev,
+                    size_t ws_bytes, void* y_dev, hipStream_t stream) {
+  if (!lora_ok(prm)) return MB_ERR_INVALID_ARG;
+  const mb_lora_params& p = *prm;
+  if (p.n_rows > 0 && (!x_dev || !w_dev || !lora_a_dev || !lora_b_dev || !scale_dev ||
+                       !adapter_dev || !ws_dev || !y_dev))
+    return MB_ERR_INVALID_ARG;
+  if (!aligned16(x_dev) || !aligned16(w_dev) || !aligned16(lora_a_dev) || !aligned16(lora_b_dev) ||
+      !aligned4(scale_dev) || !aligned4(adapter_dev) || !aligned16(ws_dev) || !aligned16(y_dev))
+    return MB_ERR_INVALID_ARG;
+  const size_t need = mb_lora_workspace_bytes(prm);
+  if (p.n_rows > 0 && ws_bytes < need) return MB_ERR_WORKSPACE;
+  const int64_t any = p.n_rows > 0, n = p.n_out, k = p.k_in, low = (int64_t)p.n_adapters * p.rank;
+  if (!outputs_apart({{y_dev, p.n_rows * n * elt_bytes(p.dtype_out), true},
+                      {ws_dev, any * (int64_t)need, true},
+                      {x_dev, p.n_rows * k * 2, false},
+                      {w_dev, any * n * k * 2, false},
+                      {lora_a_dev, any * low * k * 2, false},
+                      {lora_b_dev, any * low * n * 2, false},
+                      {scale_dev, any * p.n_adapters * 4, false},
+                      {adapter_dev, (int64_t)p.n_rows * 4, false}}))
+    return MB_ERR_INVALID_ARG;
+  return launch_project_lora(p, x_dev, w_dev, lora_a_dev, lora_b_dev, scale_dev, adapter_dev,
+                             static_cast<float*>(ws_dev), y_dev, stream) == hipSuccess
+             ? MB_OK
+             : MB_ERR_HIP;
+}
+
 int mb_plan_status(const mb_plan_bufs* plan, hipStream_t stream, int32_t host_status[4]) {
   if (!plan || !plan->status || !host_status) return MB_ERR_INVALID_ARG;
   if (hipMemcpyAsync(host_status, plan->status, 4 * sizeof(int32_t), hipMemcpyDeviceToHost,

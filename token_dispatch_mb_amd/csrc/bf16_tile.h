@@ -53,7 +53,8 @@ enum TileMode {
   kTileGated,     // silu(gate) up of a[p] w[e]^T, w's rows being gate, then up
   kTileRowGrad,   // y[p] = a[p] w[e]
   kTileGateGrad,  // the same, times the activation's derivatives at pre[p]
-  kTileWeightGrad // y[e] = sum over e's rows of a[p]^T w[p]
+  kTileWeightGrad, // y[e] = sum over e's rows of a[p]^T w[p]
+  kTileLora       // y[t] = a[t] w^T + v[t] b[adapter[t]]^T
 };
 
 struct TileArgs {
@@ -68,11 +69,53 @@ struct TileArgs {
   int n;  // columns of the output
   int k;  // length of the reduction; kTileWeightGrad: rows of the output
   int add;  // kTileWeightGrad: add to y
+  // kTileLora: one slot of `cap` rows
+  const float* v;          // [parts][cap][rank], whose sum over the parts counts
+  const uint16_t* b;       // [L][n][rank]
+  const int32_t* adapter;  // [cap]
+  int rank, L, parts;
 };
 
-// silu(g) and its derivative. exp(-g) passes binary32 where g is below -88,
-// and both go to their limit 0 there.
-__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + __expf(-g)); }
+// The adapter of a row; none (INT32_MAX) where its number is not one.
+__device__ __forceinline__ int adapter_of(const TileArgs& p, int row) {
+  const int a = p.adapter[row];
+  return (unsigned)a < (unsigned)p.L ? a : INT32_MAX;
+}
+
+// Elements [at, at + 8) of a row of v, in two bf16 that together hold 16 bits
+// of each: v's own rounding then stays below the products' other errors.
+__device__ __forceinline__ void load_v(const TileArgs& p, int row, int at, bool on, i32x4& hi,
+                                       i32x4& lo) {
+  float s[8] = {};
+  if (on && at < p.rank)
+    for (int i = 0; i < p.parts; ++i) {
+      float v[8];
+      load8<false>(p.v + ((size_t)i * p.cap + row) * p.rank + at, 0, v);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) s[x] += v[x];
+    }
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const uint32_t u = bf16x2_rne(s[2 * x], s[2 * x + 1]);
+    hi[x] = (int)u;
+    lo[x] = (int)bf16x2_rne(s[2 * x] - __uint_as_float(u << 16),
+                            s[2 * x + 1] - __uint_as_float(u & 0xffff0000u));
+  }
+}
+
+// sigmoid(g) as a product of two factors, and 1 - sigmoid(g), from t =
+// exp(-|g| / 2): exp(g) alone falls below the normal numbers at -87.3, where
+// g * exp(g) is still one.
+struct Sigmoid {
+  float a, b, rest;
+  __device__ __forceinline__ explicit Sigmoid(float g) {
+    const float t = __expf(-0.5f * fabsf(g)), q = t * t, r = __builtin_amdgcn_rcpf(1.0f + q);
+    a = g < 0 ? t : 1.0f;
+    b = g < 0 ? t * r : r;
+    rest = g < 0 ? r : q * r;
+  }
+  __device__ __forceinline__ float times(float v) const { return v * a * b; }
+};
 
 __device__ __forceinline__ f32x16 mfma_bf16(i32x4 a, i32x4 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
@@ -124,14 +167,197 @@ struct alignas(16) BfTileLds {
   uint8_t a[2][64 * JT * 128];
 };
 
-// The rows of every slot and the slots of every expert, for sums over an
-// expert's rows.
+// The rows of every slot, and of every expert the slots with rows, for sums
+// over an expert's rows.
 struct ExpertLists {
   int lo[kMaxPlanSlots];
   int n[kMaxPlanSlots];
-  int next[kMaxPlanSlots];  // the next slot of the same expert, -1: none
+  int stages[kMaxExperts];       // of an expert's sum; one, of zeros, without rows
+  int16_t next[kMaxPlanSlots];   // the expert's next slot with rows, -1: none
+  int16_t first[kMaxExperts];    // its first, -1: none
 };
 
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// The lists of the plan: an expert's home slot, then its replicas in
+// ascending order.
+template <class Args>
+__device__ void expert_lists(const Args& p, int nslots, ExpertLists& t) {
+  for (int j = threadIdx.x; j < nslots; j += kExpertThreads) {
+    int lo, hi, e;
+    slot_rows(p, j, lo, hi, e);
+    t.lo[j] = lo;
+    t.n[j] = hi - lo;
+    t.next[j] = hi > lo ? e : -1;  // its expert, for now
+  }
+  __syncthreads();
+  // the first replica slot of e from the q-th on
+  auto replica = [&](int e, int q) {
+    for (; q < p.P * p.R; ++q) {
+      const int s = q / p.R * p.NS + p.Eh + q % p.R;
+      if (t.next[s] == e) return s;
+    }
+    return -1;
+  };
+  constexpr int kEach = kMaxPlanSlots / kExpertThreads;
+  int next[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int j = threadIdx.x + i * kExpertThreads;
+    next[i] = -1;
+    if (j >= nslots) continue;
+    const int rank = j / p.NS, at = j - rank * p.NS;
+    if (at < p.Eh)
+      next[i] = replica(rank * p.Eh + at, 0);
+    else if (t.next[j] >= 0)
+      next[i] = replica(t.next[j], rank * p.R + at - p.Eh + 1);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int j = threadIdx.x + i * kExpertThreads;
+    if (j < nslots) t.next[j] = next[i];
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += kExpertThreads) {
+    const int rank = e / p.Eh, home = rank * p.NS + e - rank * p.Eh;
+    const int first = t.n[home] ? home : t.next[home];
+    int s = 0;
+    for (int j = first; j >= 0; j = t.next[j]) s += (t.n[j] + 63) / 64;
+    t.first[e] = first;
+    t.stages[e] = max(s, 1);
+  }
+  __syncthreads();
+}
+
+// ---- few rows: operands straight from memory --------------------------------
+//
+// The columns' operand is read once, and sets the pace. A workgroup computes
+// 16 outputs of 16 RT rows; its four waves take a quarter of the reduction
+// each, 128 elements at a time by turns, so that 16 rows of 1 KB are in flight,
+// and add up in LDS. v_mfma_f32_16x16x32_bf16: a lane (r = lane % 16, g = lane
+// / 16) holds elements 8g.. of row r of 32, and ends with outputs 4g.. of row r.
+__device__ __forceinline__ f32x4 mfma_few(i32x4 a, i32x4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                 __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+constexpr int kFewStep = 128;
+
+template <int kMode, bool kBF16, int RT>
+__global__ __launch_bounds__(kExpertThreads) void k_bf16_few(TileArgs p) {
+  constexpr bool kLora = kMode == kTileLora, kGated = kMode == kTileGated;
+  constexpr int NG = kGated ? 2 : 1;  // weight rows to an output
+  constexpr int U = kFewStep / 32;
+  __shared__ f32x4 sums[4][NG * RT][64];
+  __shared__ int first[kLora ? 1 : kMaxPlanSlots + 1];
+  __shared__ int part[kExpertThreads / 64];
+  if (!kLora && (p.status[0] & MB_ST_FATAL)) return;
+  const int nslots = p.P * p.NS;
+  if constexpr (!kLora) tile_table<16 * RT>(p, nslots, first, part);
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int ntn = (p.n + 15) / 16;
+  const int64_t total =
+      (int64_t)(kLora ? (p.cap + 16 * RT - 1) / (16 * RT) : first[nslots]) * ntn;
+  for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
+    const int mt = (int)(t / ntn), n0 = (int)(t - (int64_t)mt * ntn) * 16;
+    int lo = 0, hi = p.cap, e = 0, m0 = mt * 16 * RT;
+    if constexpr (!kLora) {
+      const int j = slot_of(first, nslots, mt);
+      slot_rows(p, j, lo, hi, e);
+      m0 = lo + (mt - first[j]) * 16 * RT;
+    }
+    // rows past the slot's or the weights' end read the last one instead
+    const uint16_t *w[NG], *a[RT];
+#pragma unroll
+    for (int i = 0; i < NG; ++i)
+      w[i] = p.w + (((int64_t)e * NG + i) * p.n + min(n0 + r, p.n - 1)) * p.k + g * 8;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) a[i] = p.a + (int64_t)min(m0 + i * 16 + r, hi - 1) * p.k + g * 8;
+    f32x4 acc[NG * RT] = {};
+    int k = wave * kFewStep;
+    for (; k + kFewStep <= p.k; k += 4 * kFewStep) {
+      i32x4 wv[NG][U], av[RT][U];
+#pragma unroll
+      for (int i = 0; i < NG; ++i)
+#pragma unroll
+        for (int u = 0; u < U; ++u) wv[i][u] = load16(w[i] + k + u * 32);
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int u = 0; u < U; ++u) av[i][u] = load16(a[i] + k + u * 32);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int o = 0; o < NG; ++o)
+            acc[i * NG + o] = mfma_few(wv[o][u], av[i][u], acc[i * NG + o]);
+    }
+    for (; k < p.k; k += 32) {  // the wave whose turn the rest of the rows is
+      const bool in = k + g * 8 < p.k;
+      i32x4 wv[NG];
+#pragma unroll
+      for (int o = 0; o < NG; ++o) wv[o] = in ? load16(w[o] + k) : i32x4{};
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const i32x4 av = in ? load16(a[i] + k) : i32x4{};
+#pragma unroll
+        for (int o = 0; o < NG; ++o) acc[i * NG + o] = mfma_few(wv[o], av, acc[i * NG + o]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NG * RT; ++i) sums[wave][i][lane] = acc[i];
+    __syncthreads();
+    for (int i = wave; i < RT; i += 4) {
+      f32x4 o[NG];
+#pragma unroll
+      for (int q = 0; q < NG; ++q)
+        o[q] = (sums[0][i * NG + q][lane] + sums[1][i * NG + q][lane]) +
+               (sums[2][i * NG + q][lane] + sums[3][i * NG + q][lane]);
+      const int m = m0 + i * 16 + r, nn = n0 + 4 * g;
+      if constexpr (kLora) {
+        const int row = min(m, hi - 1), id = adapter_of(p, row);
+        for (int ad = -1;;) {
+          ad = wave_min_i32(id > ad ? id : INT32_MAX);
+          if (ad == INT32_MAX) break;
+          for (int q = 0; q < p.rank; q += 32) {
+            const int at = q + g * 8;
+            i32x4 b = {}, vh, vl;
+            if (n0 + r < p.n && at < p.rank)
+              b = load16(p.b + ((size_t)ad * p.n + n0 + r) * p.rank + at);
+            load_v(p, row, at, id == ad, vh, vl);
+            o[0] = mfma_few(b, vh, o[0]);
+            o[0] = mfma_few(b, vl, o[0]);
+          }
+        }
+      }
+      if (m < hi && nn < p.n) {
+        if constexpr (kGated) {
+          float h[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) h[x] = Sigmoid(o[0][x]).times(o[0][x]) * o[NG - 1][x];
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + (size_t)m * p.n + nn) =
+              uint2{bf16x2_rne(h[0], h[1]), bf16x2_rne(h[2], h[3])};
+          if (p.pre)
+#pragma unroll
+            for (int q = 0; q < NG; ++q)
+              *reinterpret_cast<uint2*>(p.pre + ((size_t)m * NG + q) * p.n + nn) =
+                  uint2{bf16x2_rne(o[q][0], o[q][1]), bf16x2_rne(o[q][2], o[q][3])};
+        } else if constexpr (kBF16) {
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + (size_t)m * p.n + nn) =
+              uint2{bf16x2_rne(o[0][0], o[0][1]), bf16x2_rne(o[0][2], o[0][3])};
+        } else {
+          *reinterpret_cast<f32x4*>(static_cast<float*>(p.y) + (size_t)m * p.n + nn) = o[0];
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ---- tiles staged through LDS ------------------------------------------------
 struct BfTile {
   int m0, hi, n0, e;
 };
@@ -139,14 +365,15 @@ struct BfTile {
 template <int kMode, bool kBF16, int JT>
 __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
   constexpr int BM = 64 * JT, JH = JT / 2;
-  constexpr bool kColW = kMode >= kTileRowGrad, kColA = kMode == kTileWeightGrad;
+  constexpr bool kLora = kMode == kTileLora;
+  constexpr bool kColW = kMode >= kTileRowGrad && !kLora, kColA = kMode == kTileWeightGrad;
   constexpr bool kSum = kMode == kTileWeightGrad;
   constexpr int BN = kMode == kTileGated ? kTileN / 2 : kTileN;  // outputs of a tile's columns
   static_assert(BM <= kMaxTileRows, "rows behind a tile's last are numbered in int32");
   __shared__ BfTileLds<JT> lds;
   __shared__ typename std::conditional<kSum, ExpertLists, int[kMaxPlanSlots + 1]>::type table;
   __shared__ int part[kExpertThreads / 64];
-  if (p.status[0] & MB_ST_FATAL) return;
+  if (!kLora && (p.status[0] & MB_ST_FATAL)) return;
   const int nslots = p.P * p.NS;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 31, h = lane >> 5;
@@ -154,41 +381,12 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
   const int ntn = (p.n + BN - 1) / BN;
   int mtiles = 0, total = 0;  // row tiles (of an expert, where it sums), tiles
   if constexpr (kSum) {
-    for (int j = threadIdx.x; j < nslots; j += kExpertThreads) {
-      int lo, hi, e;
-      slot_rows(p, j, lo, hi, e);
-      table.lo[j] = lo;
-      table.n[j] = hi - lo;
-      table.next[j] = hi > lo ? e : -1;  // its expert, for now
-    }
-    __syncthreads();
-    // an expert's home slot, then its replicas in ascending order
-    constexpr int kEach = kMaxPlanSlots / kExpertThreads;
-    int nx[kEach];
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int j = threadIdx.x + i * kExpertThreads;
-      nx[i] = -1;
-      if (j >= nslots) continue;
-      const int rank = j / p.NS, at = j - rank * p.NS;
-      const bool home = at < p.Eh;
-      const int e = home ? rank * p.Eh + at : table.next[j];
-      if (e < 0) continue;
-      for (int q = home ? 0 : rank * p.R + at - p.Eh + 1; q < p.P * p.R; ++q) {
-        const int s = q / p.R * p.NS + p.Eh + q % p.R;
-        if (table.next[s] == e) {
-          nx[i] = s;
-          break;
-        }
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      if (threadIdx.x + i * kExpertThreads < nslots) table.next[threadIdx.x + i * kExpertThreads] = nx[i];
-    __syncthreads();
+    expert_lists(p, nslots, table);
     mtiles = (p.k + BM - 1) / BM;
     total = mtiles * ntn * p.E;
+  } else if constexpr (kLora) {
+    mtiles = (p.cap + BM - 1) / BM;
+    total = mtiles * ntn;
   } else {
     tile_table<BM>(p, nslots, table, part);
     mtiles = __builtin_amdgcn_readfirstlane(table[nslots]);
@@ -214,6 +412,10 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
       o.m0 = mt * BM;
       o.hi = p.k;
       o.e = e;
+    } else if constexpr (kLora) {
+      o.m0 = mt * BM;
+      o.hi = p.cap;
+      o.e = 0;
     } else {
       const int j = slot_of(table, nslots, mt);
       int lo;
@@ -222,28 +424,11 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
     }
     return o;
   };
-  // kSum: the first slot of the list from j that holds rows
-  auto with_rows = [&](int j) {
-    if constexpr (kSum)
-      while (j >= 0 && !__builtin_amdgcn_readfirstlane(table.n[j]))
-        j = __builtin_amdgcn_readfirstlane(table.next[j]);
-    return j;
-  };
-  auto home_of = [&](int e) {
-    const int rank = e / p.Eh;
-    return rank * p.NS + e - rank * p.Eh;
-  };
-  // stages of a tile; a sum over no rows takes one, of zeros
   auto stages_of = [&](int e) {
-    if constexpr (kSum) {
-      int s = 0;
-      for (int j = with_rows(home_of(e)); j >= 0;
-           j = with_rows(__builtin_amdgcn_readfirstlane(table.next[j])))
-        s += (__builtin_amdgcn_readfirstlane(table.n[j]) + 63) / 64;
-      return max(s, 1);
-    } else {
+    if constexpr (kSum)
+      return uniform(table.stages[e]);
+    else
       return (p.k + 63) / 64;
-    }
   };
   if (tile_index(0) >= total) return;
   const int tiles = (total - tile_index(0) + gridDim.x - 1) / gridDim.x;
@@ -289,10 +474,15 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
   Operand<kColW> ow;
   Operand<kColA> oa;
   int c_it = 0, c_left = 0, c_buf = 0, c_slot = 0, c_n0 = 0, c_m0 = 0;
-  // kSum: `rows` rows from `at` on
-  auto sum_at = [&](int64_t at, int rows) {
-    ow = {p.w + (at + wave * 16) * p.n + c_n0, rows - wave * 16, c_n0};
-    oa = {p.a + (at + wave * 16) * p.k + c_m0, rows - wave * 16, c_m0};
+  // kSum: the rows of slot j, none where it is negative
+  auto sum_slot = [&](int j) {
+    if constexpr (kSum) {
+      c_slot = j;
+      const int at = uniform(j < 0 ? 0 : table.lo[j]) + wave * 16;
+      const int rows = uniform(j < 0 ? 0 : table.n[j]) - wave * 16;
+      ow = {p.w + (int64_t)at * p.n + c_n0, rows, c_n0};
+      oa = {p.a + (int64_t)at * p.k + c_m0, rows, c_m0};
+    }
   };
   auto aim = [&](int it) {
     const BfTile t = tile_of(tile_index(it));
@@ -300,12 +490,7 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
     if constexpr (kSum) {
       c_n0 = t.n0;
       c_m0 = t.m0;
-      c_slot = with_rows(home_of(t.e));
-      if (c_slot >= 0)
-        sum_at(__builtin_amdgcn_readfirstlane(table.lo[c_slot]),
-               __builtin_amdgcn_readfirstlane(table.n[c_slot]));
-      else
-        sum_at(0, 0);
+      sum_slot(uniform(table.first[t.e]));
     } else {
       const int m = t.m0 + wave * 16 * JT, nm = min(max(t.hi - m, 0), 16 * JT);
       oa = {p.a + (int64_t)m * p.k, nm * pa, 0};
@@ -334,11 +519,7 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
       ow.next(pw);
       oa.next(pa);
       if constexpr (kSum) {
-        if (ow.left + wave * 16 <= 0) {  // the next of the expert's slots
-          c_slot = with_rows(__builtin_amdgcn_readfirstlane(table.next[c_slot]));
-          sum_at(__builtin_amdgcn_readfirstlane(table.lo[c_slot]),
-                 __builtin_amdgcn_readfirstlane(table.n[c_slot]));
-        }
+        if (ow.left + wave * 16 <= 0) sum_slot(uniform(table.next[c_slot]));
       }
     }
   };
@@ -465,6 +646,44 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
       }
       next_stage();
     }
+    if constexpr (kLora) {
+      // the reduction goes on over the ranks of every adapter among the
+      // wave's rows, with zeros in the rows of the others
+      int row[JN], id[JN];
+#pragma unroll
+      for (int j = 0; j < JN; ++j) {
+        row[j] = min(tile.m0 + (2 * j + hm) * 32 + r, tile.hi - 1);
+        id[j] = adapter_of(p, row[j]);
+      }
+      for (int ad = -1;;) {
+        int least = INT32_MAX;
+#pragma unroll
+        for (int j = 0; j < JN; ++j)
+          if (id[j] > ad) least = min(least, id[j]);
+        ad = wave_min_i32(least);
+        if (ad == INT32_MAX) break;
+        for (int q = 0; q < p.rank; q += 16) {
+          const int at = q + h * 8;
+          i32x4 b[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int n = tile.n0 + hn * 128 + i * 32 + ((r & 19) | ((r & 4) << 1) | ((r & 8) >> 1));
+            b[i] = i32x4{};
+            if (n < p.n && at < p.rank) b[i] = load16(p.b + ((size_t)ad * p.n + n) * p.rank + at);
+          }
+#pragma unroll
+          for (int j = 0; j < JN; ++j) {
+            i32x4 hi, lo;
+            load_v(p, row[j], at, id[j] == ad, hi, lo);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              acc[i][j] = mfma_bf16(b[i], hi, acc[i][j]);
+              acc[i][j] = mfma_bf16(b[i], lo, acc[i][j]);
+            }
+          }
+        }
+      }
+    }
     // ---- the outputs ----
 #pragma unroll
     for (int j = 0; j < JN; ++j) {
@@ -482,7 +701,7 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
             for (int x = 0; x < 8; ++x) {
               g[x] = acc[i][j][v + x];
               u[x] = acc[i + 2][j][v + x];
-              o[x] = g[x] * sigmoid(g[x]) * u[x];
+              o[x] = Sigmoid(g[x]).times(g[x]) * u[x];
             }
             if (row && nn < p.n) {
               store8_at<true>(p.y, (size_t)m * p.n + nn, o);
@@ -511,9 +730,9 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
               load8<true>(p.pre + (size_t)m * 2 * p.n + p.n + nn, 0, u);
 #pragma unroll
               for (int x = 0; x < 8; ++x) {
-                const float s = sigmoid(g[x]);
-                du[x] = o[x] * g[x] * s;
-                o[x] = o[x] * u[x] * s * (1.0f + g[x] * (1.0f - s));
+                const Sigmoid s(g[x]);
+                du[x] = s.times(o[x] * g[x]);
+                o[x] = s.times(o[x] * u[x]) * (1.0f + g[x] * s.rest);
               }
               store8_at<true>(p.y, (size_t)m * 2 * p.n + nn, o);
               store8_at<true>(p.y, (size_t)m * 2 * p.n + p.n + nn, du);

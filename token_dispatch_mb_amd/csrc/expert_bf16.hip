@@ -6,6 +6,8 @@
 namespace mb {
 namespace {
 
+constexpr int kFewGroups = 2048;
+
 TileArgs plan_args(const mb_dims& d, const Geometry& g, const mb_plan_bufs& o) {
   TileArgs p = {};
   p.cu = o.cu_seqlens;
@@ -22,6 +24,12 @@ void launch_tiles(const TileArgs& p, int64_t rows, hipStream_t st) {
   const int64_t slots = (int64_t)p.P * p.NS;
   const int64_t columns = (p.n + kTileN - 1) / kTileN;
   const dim3 grid(kCus), block(kExpertThreads);
+  if constexpr (kMode == kTileProduct || kMode == kTileGated) {
+    if (rows < slots * 2) {
+      hipLaunchKernelGGL((k_bf16_few<kMode, kBF16, 1>), dim3(kFewGroups), block, 0, st, p);
+      return;
+    }
+  }
   if (rows >= slots * 160 && (rows / 256 + slots) * columns > 2 * kCus)
     hipLaunchKernelGGL((k_bf16_tile<kMode, kBF16, 4>), grid, block, 0, st, p);
   else

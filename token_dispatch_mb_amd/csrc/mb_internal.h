@@ -22,6 +22,8 @@ constexpr int kMaxGroups = 64;             // one wave lane per group in k_route
 constexpr int kMaxWaves = (1 << 26) - 16;  // waves of one launch: fewer than 2^32 threads
 constexpr int kMaxExpertDim = 1 << 20;     // n_out and k_in of the experts' products
 constexpr int kMaxTileRows = 256;          // rows of one of their tiles at most
+constexpr int kMaxLoraRows = 1 << 26;      // one 16-row block to a workgroup of 256 threads
+constexpr int kMaxAdapters = 1 << 20;
 // Block-count tables k_plan and k_assign sum directly instead of running
 // k_scan: at most this many routing blocks per source and block counts.
 constexpr int kSmallTableBlocks = 4;
@@ -148,6 +150,15 @@ hipError_t launch_expert_bf16_wgrad(const mb_dims& d, const Geometry& g, const m
                                     int32_t n_out, int32_t k_in, bool add, bool bf16,
                                     const uint16_t* dy, const uint16_t* a, void* dw,
                                     hipStream_t st);
+// dye or dw may be NULL: not wanted.
+hipError_t launch_combine_grad(const mb_dims& d, const mb_plan_bufs& o, const void* dy,
+                               const void* ye, const float* w, void* dye, float* dw,
+                               hipStream_t st);
+// v: lora_parts(p) * rows * rank floats of scratch.
+int lora_parts(const mb_lora_params& p);
+hipError_t launch_project_lora(const mb_lora_params& p, const uint16_t* x, const uint16_t* w,
+                               const uint16_t* a, const uint16_t* b, const float* scale,
+                               const int32_t* adapter, float* v, void* y, hipStream_t st);
 
 // Launch KERNEL<K> for the top-K values with a specialised kernel, KERNEL<0>
 // (runtime K) otherwise.
