@@ -54,12 +54,13 @@ enum TileMode {
   kTileRowGrad,   // y[p] = a[p] w[e]
   kTileGateGrad,  // the same, times the activation's derivatives at pre[p]
   kTileWeightGrad, // y[e] = sum over e's rows of a[p]^T w[p]
+  kTileWeightAdd,  // the same, added to y
   kTileLora       // y[t] = a[t] w^T + v[t] b[adapter[t]]^T
 };
 
 struct TileArgs {
   const uint16_t* a;  // the rows
-  const uint16_t* w;  // the columns: weights, or (kTileWeightGrad) rows
+  const uint16_t* w;  // the columns: weights, or (weights' gradient) rows
   void* y;
   uint16_t* pre;
   const int32_t* cu;
@@ -67,8 +68,7 @@ struct TileArgs {
   const int32_t* status;
   int P, E, Eh, NS, R, cap;
   int n;  // columns of the output
-  int k;  // length of the reduction; kTileWeightGrad: rows of the output
-  int add;  // kTileWeightGrad: add to y
+  int k;  // length of the reduction; weights' gradient: rows of the output
   // kTileLora: one slot of `cap` rows
   const float* v;          // [parts][cap][rank], whose sum over the parts counts
   const uint16_t* b;       // [L][n][rank]
@@ -82,10 +82,9 @@ __device__ __forceinline__ int adapter_of(const TileArgs& p, int row) {
   return (unsigned)a < (unsigned)p.L ? a : INT32_MAX;
 }
 
-// Elements [at, at + 8) of a row of v, in two bf16 that together hold 16 bits
-// of each: v's own rounding then stays below the products' other errors.
-__device__ __forceinline__ void load_v(const TileArgs& p, int row, int at, bool on, i32x4& hi,
-                                       i32x4& lo) {
+// Elements [at, at + 8) of a row of v, each as three bf16 that together hold
+// all of its 24 bits: v is not rounded.
+__device__ __forceinline__ void load_v(const TileArgs& p, int row, int at, bool on, i32x4* v3) {
   float s[8] = {};
   if (on && at < p.rank)
     for (int i = 0; i < p.parts; ++i) {
@@ -95,27 +94,81 @@ __device__ __forceinline__ void load_v(const TileArgs& p, int row, int at, bool 
       for (int x = 0; x < 8; ++x) s[x] += v[x];
     }
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    const uint32_t u = bf16x2_rne(s[2 * x], s[2 * x + 1]);
-    hi[x] = (int)u;
-    lo[x] = (int)bf16x2_rne(s[2 * x] - __uint_as_float(u << 16),
-                            s[2 * x + 1] - __uint_as_float(u & 0xffff0000u));
-  }
+  for (int q = 0; q < 3; ++q)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const uint32_t a = __float_as_uint(s[2 * x]) & 0xffff0000u;
+      const uint32_t b = __float_as_uint(s[2 * x + 1]) & 0xffff0000u;
+      v3[q][x] = (int)(a >> 16 | b);
+      // nothing is left of an infinity or a NaN
+      s[2 * x] = fabsf(s[2 * x]) < INFINITY ? s[2 * x] - __uint_as_float(a) : 0.0f;
+      s[2 * x + 1] = fabsf(s[2 * x + 1]) < INFINITY ? s[2 * x + 1] - __uint_as_float(b) : 0.0f;
+    }
 }
 
-// sigmoid(g) as a product of two factors, and 1 - sigmoid(g), from t =
-// exp(-|g| / 2): exp(g) alone falls below the normal numbers at -87.3, where
-// g * exp(g) is still one.
+// sigmoid(g) as a product of two factors, and 1 - sigmoid(g). kFar: from t =
+// exp(-|g| / 2), since 1 / (1 + exp(-g)) falls below the normal numbers at
+// -87.3, where g * sigmoid(g) is still one.
+template <bool kFar>
 struct Sigmoid {
   float a, b, rest;
   __device__ __forceinline__ explicit Sigmoid(float g) {
-    const float t = __expf(-0.5f * fabsf(g)), q = t * t, r = __builtin_amdgcn_rcpf(1.0f + q);
-    a = g < 0 ? t : 1.0f;
-    b = g < 0 ? t * r : r;
-    rest = g < 0 ? r : q * r;
+    if constexpr (kFar) {
+      const float t = __expf(-0.5f * fabsf(g)), q = t * t, r = __builtin_amdgcn_rcpf(1.0f + q);
+      a = g < 0 ? t : 1.0f;
+      b = g < 0 ? t * r : r;
+      rest = g < 0 ? r : q * r;
+    } else {
+      a = 1.0f;
+      b = __builtin_amdgcn_rcpf(1.0f + __expf(-g));
+      rest = 1.0f - b;
+    }
   }
-  __device__ __forceinline__ float times(float v) const { return v * a * b; }
+  __device__ __forceinline__ float times(float v) const { return kFar ? v * a * b : v * b; }
 };
+
+// Whether one of the wave's gates is that far (every lane active).
+template <int N>
+__device__ __forceinline__ bool far_gate(const float* g) {
+  float least = g[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) least = fminf(least, g[i]);
+  return __ballot(least < -80.0f) != 0;
+}
+
+// o = silu(g) u
+template <int N, bool kFar>
+__device__ __forceinline__ void gate_of(const float* g, const float* u, float* o) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) o[i] = Sigmoid<kFar>(g[i]).times(g[i]) * u[i];
+}
+
+template <int N>
+__device__ __forceinline__ void gated(const float* g, const float* u, float* o) {
+  if (far_gate<N>(g))
+    gate_of<N, true>(g, u, o);
+  else
+    gate_of<N, false>(g, u, o);
+}
+
+// From d, the gradient of silu(g) u: those of g (in place) and of u.
+template <int N, bool kFar>
+__device__ __forceinline__ void gate_grad_of(const float* g, const float* u, float* d, float* du) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const Sigmoid<kFar> s(g[i]);
+    du[i] = s.times(d[i] * g[i]);
+    d[i] = s.times(d[i] * u[i]) * fmaf(g[i], s.rest, 1.0f);
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void gate_grad(const float* g, const float* u, float* d, float* du) {
+  if (far_gate<N>(g))
+    gate_grad_of<N, true>(g, u, d, du);
+  else
+    gate_grad_of<N, false>(g, u, d, du);
+}
 
 __device__ __forceinline__ f32x16 mfma_bf16(i32x4 a, i32x4 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
@@ -128,20 +181,6 @@ __device__ __forceinline__ i32x4 read_tr(const uint8_t* lo, const uint8_t* hi) {
   const i32x2 a = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr)lo));
   const i32x2 b = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr)hi));
   return i32x4{a[0], a[1], b[0], b[1]};
-}
-
-// Eight consecutive elements of an output row.
-template <bool kBF16>
-__device__ __forceinline__ void store8_at(void* y, size_t at, const float* v) {
-  if constexpr (kBF16) {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + at) =
-        uint4{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]),
-              bf16x2_rne(v[6], v[7])};
-  } else {
-    f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(y) + at);
-    o[0] = f32x4{v[0], v[1], v[2], v[3]};
-    o[1] = f32x4{v[4], v[5], v[6], v[7]};
-  }
 }
 
 // What the copies of one operand read in a stage. kRows: `left` bytes from
@@ -167,6 +206,14 @@ struct alignas(16) BfTileLds {
   uint8_t a[2][64 * JT * 128];
 };
 
+// The rows of every slot and its expert (-1: no rows), and the row tiles of
+// the slots before it.
+struct SlotTable {
+  int first[kMaxPlanSlots + 1];
+  int lo[kMaxPlanSlots], hi[kMaxPlanSlots];
+  int16_t e[kMaxPlanSlots];
+};
+
 // The rows of every slot, and of every expert the slots with rows, for sums
 // over an expert's rows.
 struct ExpertLists {
@@ -178,6 +225,30 @@ struct ExpertLists {
 };
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+template <int BM, class Args>
+__device__ void slot_table(const Args& p, int nslots, SlotTable& t, int* part) {
+  tile_table<BM>(p, nslots, t.first, part);
+  for (int j = threadIdx.x; j < nslots; j += kExpertThreads) {
+    int lo, hi, e;
+    slot_rows(p, j, lo, hi, e);
+    t.lo[j] = lo;
+    t.hi[j] = hi;
+    t.e[j] = hi > lo ? e : -1;
+  }
+  __syncthreads();
+}
+
+// The slot whose tiles hold row tile t: the last whose first tile is not
+// behind t, found in two reads by the wave.
+__device__ __forceinline__ int slot_at(const SlotTable& s, int nslots, int t, int lane) {
+  constexpr int kEach = kMaxPlanSlots / 64;
+  const int a = lane * kEach;
+  const int group = __builtin_popcountll(__ballot(a < nslots && s.first[a] <= t)) - 1;
+  const int b = group * kEach + lane;
+  return group * kEach - 1 +
+         __builtin_popcountll(__ballot(lane < kEach && b < nslots && s.first[b] <= t));
+}
 
 // The lists of the plan: an expert's home slot, then its replicas in
 // ascending order.
@@ -317,6 +388,12 @@ __global__ __launch_bounds__(kExpertThreads) void k_bf16_few(TileArgs p) {
         o[q] = (sums[0][i * NG + q][lane] + sums[1][i * NG + q][lane]) +
                (sums[2][i * NG + q][lane] + sums[3][i * NG + q][lane]);
       const int m = m0 + i * 16 + r, nn = n0 + 4 * g;
+      float h[4];
+      if constexpr (kGated) {
+        const float x[4] = {o[0][0], o[0][1], o[0][2], o[0][3]};
+        const float u[4] = {o[1][0], o[1][1], o[1][2], o[1][3]};
+        gated<4>(x, u, h);
+      }
       if constexpr (kLora) {
         const int row = min(m, hi - 1), id = adapter_of(p, row);
         for (int ad = -1;;) {
@@ -324,20 +401,17 @@ __global__ __launch_bounds__(kExpertThreads) void k_bf16_few(TileArgs p) {
           if (ad == INT32_MAX) break;
           for (int q = 0; q < p.rank; q += 32) {
             const int at = q + g * 8;
-            i32x4 b = {}, vh, vl;
+            i32x4 b = {}, v[3];
             if (n0 + r < p.n && at < p.rank)
               b = load16(p.b + ((size_t)ad * p.n + n0 + r) * p.rank + at);
-            load_v(p, row, at, id == ad, vh, vl);
-            o[0] = mfma_few(b, vh, o[0]);
-            o[0] = mfma_few(b, vl, o[0]);
+            load_v(p, row, at, id == ad, v);
+#pragma unroll
+            for (int x = 0; x < 3; ++x) o[0] = mfma_few(b, v[x], o[0]);
           }
         }
       }
       if (m < hi && nn < p.n) {
         if constexpr (kGated) {
-          float h[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) h[x] = Sigmoid(o[0][x]).times(o[0][x]) * o[NG - 1][x];
           *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + (size_t)m * p.n + nn) =
               uint2{bf16x2_rne(h[0], h[1]), bf16x2_rne(h[2], h[3])};
           if (p.pre)
@@ -362,20 +436,68 @@ struct BfTile {
   int m0, hi, n0, e;
 };
 
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+
+// An output, or what its gradient needs, from a tile's first row on. Lanes
+// behind the last row, or with a negative offset, read zeros and write
+// nothing, without a branch: every wave issues the same number of stores for
+// a tile, which the wait in the next tile's first stage counts on.
+struct RowBuffer {
+  __amdgpu_buffer_rsrc_t at;
+  __device__ __forceinline__ RowBuffer(void* p, int rows, int pitch)
+      : at(__builtin_amdgcn_make_buffer_rsrc(scalar(p), 0, uniform(max(rows, 0) * pitch),
+                                             0x00020000)) {}
+  static __device__ __forceinline__ void* scalar(void* p) {
+    const uint64_t at = reinterpret_cast<uint64_t>(p);
+    return reinterpret_cast<void*>((uint64_t)(uint32_t)uniform((int)(at >> 32)) << 32 |
+                                   (uint32_t)uniform((int)at));
+  }
+  __device__ __forceinline__ void store(int off, u32x4 v) const {
+    __builtin_amdgcn_raw_buffer_store_b128(v, at, off, 0, 0);
+  }
+  __device__ __forceinline__ u32x4 load(int off) const {
+    return __builtin_amdgcn_raw_buffer_load_b128(at, off, 0, 0);
+  }
+  template <bool kBF16>
+  __device__ __forceinline__ void store8(int off, const float* v) const {
+    if constexpr (kBF16) {
+      store(off, u32x4{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]),
+                       bf16x2_rne(v[6], v[7])});
+    } else {
+      store(off, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                       __float_as_uint(v[3])});
+      store(off + 16, u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
+                            __float_as_uint(v[7])});
+    }
+  }
+};
+
+__device__ __forceinline__ void bf16_of(u32x4 u, float* v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(u[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+
 template <int kMode, bool kBF16, int JT>
 __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
   constexpr int BM = 64 * JT, JH = JT / 2;
-  constexpr bool kLora = kMode == kTileLora;
-  constexpr bool kColW = kMode >= kTileRowGrad && !kLora, kColA = kMode == kTileWeightGrad;
-  constexpr bool kSum = kMode == kTileWeightGrad;
-  constexpr int BN = kMode == kTileGated ? kTileN / 2 : kTileN;  // outputs of a tile's columns
+  constexpr bool kLora = kMode == kTileLora, kGated = kMode == kTileGated;
+  constexpr bool kGateGrad = kMode == kTileGateGrad, kAdd = kMode == kTileWeightAdd;
+  constexpr bool kSum = kMode == kTileWeightGrad || kAdd;
+  constexpr bool kColW = kMode == kTileRowGrad || kGateGrad || kSum, kColA = kSum;
+  constexpr int BN = kGated ? kTileN / 2 : kTileN;  // outputs of a tile's columns
+  constexpr int kElt = kBF16 ? 2 : 4;
+  // stores of a wave for 32 rows of a tile (without pre)
+  constexpr int kStores = kGated ? 4 : kGateGrad ? 16 : 8 * kElt / 2;
   static_assert(BM <= kMaxTileRows, "rows behind a tile's last are numbered in int32");
   __shared__ BfTileLds<JT> lds;
-  __shared__ typename std::conditional<kSum, ExpertLists, int[kMaxPlanSlots + 1]>::type table;
+  __shared__ typename std::conditional<kSum, ExpertLists, SlotTable>::type table;
   __shared__ int part[kExpertThreads / 64];
   if (!kLora && (p.status[0] & MB_ST_FATAL)) return;
   const int nslots = p.P * p.NS;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int r = lane & 31, h = lane >> 5;
   const int hn = wave >> 1, hm = wave & 1;
   const int ntn = (p.n + BN - 1) / BN;
@@ -388,8 +510,8 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
     mtiles = (p.cap + BM - 1) / BM;
     total = mtiles * ntn;
   } else {
-    tile_table<BM>(p, nslots, table, part);
-    mtiles = __builtin_amdgcn_readfirstlane(table[nslots]);
+    slot_table<BM>(p, nslots, table, part);
+    mtiles = uniform(table.first[nslots]);
     total = mtiles * ntn;
   }
   // workgroups go round the XCDs: those of one XCD take runs of consecutive
@@ -397,30 +519,29 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
   const int per = gridDim.x / kXcds;
   const int xcd = blockIdx.x % kXcds, local = blockIdx.x / kXcds;
   auto tile_index = [&](int it) { return (it * kXcds + xcd) * per + local; };
+  // (quotients are computed in vector registers: read back, or all that
+  // follows from them, the copies' buffers too, would be held there)
   auto tile_of = [&](int t) {
     BfTile o;
     int e = 0;
     if constexpr (kSum) {
-      e = t / (mtiles * ntn);
+      e = uniform(t / (mtiles * ntn));
       t -= e * mtiles * ntn;
     }
-    const int group = t / (kGroupM * ntn), rem = t - group * (kGroupM * ntn);
+    const int group = uniform(t / (kGroupM * ntn)), rem = t - group * (kGroupM * ntn);
     const int gm = min(kGroupM, mtiles - group * kGroupM);
-    const int mt = group * kGroupM + rem % gm;
-    o.n0 = rem / gm * BN;
-    if constexpr (kSum) {
+    const int column = uniform(rem / gm);
+    const int mt = group * kGroupM + rem - column * gm;
+    o.n0 = column * BN;
+    if constexpr (kSum || kLora) {
       o.m0 = mt * BM;
-      o.hi = p.k;
+      o.hi = kSum ? p.k : p.cap;
       o.e = e;
-    } else if constexpr (kLora) {
-      o.m0 = mt * BM;
-      o.hi = p.cap;
-      o.e = 0;
     } else {
-      const int j = slot_of(table, nslots, mt);
-      int lo;
-      slot_rows(p, j, lo, o.hi, o.e);
-      o.m0 = lo + (mt - __builtin_amdgcn_readfirstlane(table[j])) * BM;
+      const int j = slot_at(table, nslots, mt, lane);
+      o.m0 = uniform(table.lo[j]) + (mt - uniform(table.first[j])) * BM;
+      o.hi = uniform(table.hi[j]);
+      o.e = uniform(table.e[j]);
     }
     return o;
   };
@@ -474,6 +595,9 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
   Operand<kColW> ow;
   Operand<kColA> oa;
   int c_it = 0, c_left = 0, c_buf = 0, c_slot = 0, c_n0 = 0, c_m0 = 0;
+  // the tile that the copies are at, and the two before it: the product's is
+  // among them
+  BfTile at0 = {}, at1 = {}, at2 = {};
   // kSum: the rows of slot j, none where it is negative
   auto sum_slot = [&](int j) {
     if constexpr (kSum) {
@@ -486,6 +610,9 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
   };
   auto aim = [&](int it) {
     const BfTile t = tile_of(tile_index(it));
+    at2 = at1;
+    at1 = at0;
+    at0 = t;
     c_left = stages_of(t.e);
     if constexpr (kSum) {
       c_n0 = t.n0;
@@ -496,7 +623,7 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
       oa = {p.a + (int64_t)m * p.k, nm * pa, 0};
       if constexpr (kColW) {  // reduction rows, each wave its 16 of a stage
         ow = {p.w + ((int64_t)t.e * p.k + wave * 16) * p.n + t.n0, p.k - wave * 16, t.n0};
-      } else if constexpr (kMode == kTileGated) {
+      } else if constexpr (kGated) {
         // waves 0 and 2 copy gate rows, 1 and 3 the up rows of the same outputs
         const int n = t.n0 + (wave >> 1) * 64, nn = min(max(p.n - n, 0), 64);
         ow = {p.w + (((int64_t)t.e * 2 + (wave & 1)) * p.n + n) * p.k, nn * pw, 0};
@@ -509,17 +636,20 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
   auto next_stage = [&] {
     c_buf ^= 1;
     if (--c_left == 0) {
-      if (++c_it < tiles) {
+      ++c_it;
+      if (c_it < tiles) {
         aim(c_it);
         return;
       }
       ow.left = oa.left = 0;
       c_left = 1 << 30;
+      at2 = at1;
+      at1 = at0;
     } else {
       ow.next(pw);
       oa.next(pa);
       if constexpr (kSum) {
-        if (ow.left + wave * 16 <= 0) sum_slot(uniform(table.next[c_slot]));
+        if (c_it < tiles && ow.left + wave * 16 <= 0) sum_slot(uniform(table.next[c_slot]));
       }
     }
   };
@@ -545,6 +675,7 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
   i32x4 fw[4][2], fa[JT][2];
   constexpr int kPitchW = kTileN * 2, kPitchA = BM * 2;  // of reduction rows (kCols)
   const int piece = ((2 * h) ^ ((r >> 1) & 7)) << 4;     // kRows: of (step 0, h, 0)
+  const int swapped = (r & 19) | ((r & 4) << 1) | ((r & 8) >> 1);
   int at_w[4], at_a[JT];
   {
     // kCols: lane i of 16 addresses row i / 4, 4 columns; group lane / 16 % 2
@@ -556,7 +687,7 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
       at_w[t] = kColW ? (16 * h + (i >> 2)) * kPitchW +
                             (((hn * 16 + t * 4 + g * 2 + (chunk >> 1)) ^ (i >> 2 << 2)) << 4) +
                             (chunk & 1) * 8
-                      : (hn * 128 + t * 32 + ((r & 19) | ((r & 4) << 1) | ((r & 8) >> 1))) * 128;
+                      : (hn * 128 + t * 32 + swapped) * 128;
 #pragma unroll
     for (int t = 0; t < JT; ++t)
       at_a[t] = kColA ? (16 * h + (i >> 2)) * kPitchA +
@@ -600,12 +731,14 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
 
   // A tile of no more than half its rows (a slot's last) leaves the second
   // half of every wave's accumulators out, the waves' row tiles taking turns.
-  auto run = [&](const BfTile& tile, auto half_) {
+  // stored: whether the tile before was whole (2) or half (1); 0 before the
+  // first.
+  auto run = [&](const BfTile& tile, int stored, auto half_) {
     constexpr bool kHalf = decltype(half_)::value;
     constexpr int JN = kHalf ? JH : JT;
-    f32x16 acc[4][JN] = {};
-    const int stages = stages_of(tile.e);
-    for (int s = 0; s < stages; ++s) {
+    f32x16 acc[4][JN];
+    auto stage = [&](auto first_) {
+      constexpr bool kFirst = decltype(first_)::value;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const i32x4 bw = ow.buffer(pw), ba = oa.buffer(pa);
@@ -615,7 +748,8 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
         for (int c = 0; c < 8; ++c) {
           const int u = c >> 2, i = c & 3;
 #pragma unroll
-          for (int j = 0; j < JH; ++j) acc[i][j] = mfma_bf16(fw[i][u], fa[j][u], acc[i][j]);
+          for (int j = 0; j < JH; ++j)
+            acc[i][j] = mfma_bf16(fw[i][u], fa[j][u], kFirst && !e && !u ? f32x16{} : acc[i][j]);
           if (!kHalf && c < JT) read_a(buf, e, JH + (c >> 1), c & 1);
           if (e) copy_w(bw, last, c);
           __builtin_amdgcn_sched_barrier(0);
@@ -623,8 +757,23 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
         if (e) {
           // this wave has read all of the stage, and its copies of the next
           // have landed (the eight just issued are of the one after); after
-          // the barrier that holds for all waves
-          wait_barrier<8>();
+          // the barrier that holds for all waves. In a tile's first stage the
+          // stores of the tile before lie between the two, and may still be
+          // under way: at least kStores for each 32 rows, of the 63 that can
+          // be counted.
+          if constexpr (kFirst) {
+            constexpr int kWhole = JT * kStores + 8 < 63 ? JT * kStores + 8 : 63;
+            constexpr int kPart = JH * kStores + 8 < 63 ? JH * kStores + 8 : 63;
+            if (stored == 2)
+              asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kWhole) : "memory");
+            else if (stored == 1)
+              asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kPart) : "memory");
+            else
+              asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)" ::: "memory");
+            asm volatile("s_barrier" ::: "memory");
+          } else {
+            wait_barrier<8>();
+          }
           buf ^= 1;
         }
         // second half: the next step's operands are read under it, and the
@@ -633,7 +782,8 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
         for (int c = 0; c < 8; ++c) {
           const int u = c >> 2, i = c & 3;
 #pragma unroll
-          for (int j = JH; j < JN; ++j) acc[i][j] = mfma_bf16(fw[i][u], fa[j][u], acc[i][j]);
+          for (int j = JH; j < JN; ++j)
+            acc[i][j] = mfma_bf16(fw[i][u], fa[j][u], kFirst && !e && !u ? f32x16{} : acc[i][j]);
           read_w(buf, 1 - e, i, u);
           if (c < JT) read_a(buf, 1 - e, c >> 1, c & 1);
           if (e) {
@@ -645,7 +795,10 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
         if (!e) read_barrier();  // all columns of the stage are in registers
       }
       next_stage();
-    }
+    };
+    const int stages = stages_of(tile.e);
+    stage(std::true_type());
+    for (int s = 1; s < stages; ++s) stage(std::false_type());
     if constexpr (kLora) {
       // the reduction goes on over the ranks of every adapter among the
       // wave's rows, with zeros in the rows of the others
@@ -667,99 +820,117 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
           i32x4 b[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int n = tile.n0 + hn * 128 + i * 32 + ((r & 19) | ((r & 4) << 1) | ((r & 8) >> 1));
+            const int n = tile.n0 + hn * 128 + i * 32 + swapped;
             b[i] = i32x4{};
             if (n < p.n && at < p.rank) b[i] = load16(p.b + ((size_t)ad * p.n + n) * p.rank + at);
           }
 #pragma unroll
           for (int j = 0; j < JN; ++j) {
-            i32x4 hi, lo;
-            load_v(p, row[j], at, id[j] == ad, hi, lo);
+            i32x4 v[3];
+            load_v(p, row[j], at, id[j] == ad, v);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              acc[i][j] = mfma_bf16(b[i], hi, acc[i][j]);
-              acc[i][j] = mfma_bf16(b[i], lo, acc[i][j]);
-            }
+            for (int x = 0; x < 3; ++x)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[i][j] = mfma_bf16(b[i], v[x], acc[i][j]);
           }
         }
       }
     }
-    // ---- the outputs ----
+    // ---- the outputs: 8 consecutive ones of a row at a time ----
+    const int rows = min(tile.hi - tile.m0, BM);
+    const int row0 = hm * 32 + r;  // + 64 j
+    if constexpr (kGated) {
+      // accumulators 0, 1 are gates, 2, 3 the same outputs' ups
+      const int pitch = p.n * 2;
+      const RowBuffer y(static_cast<uint16_t*>(p.y) + (size_t)tile.m0 * p.n, rows, pitch);
+      const RowBuffer pre(p.pre + (size_t)tile.m0 * 2 * p.n, p.pre ? rows : 0, 2 * pitch);
 #pragma unroll
-    for (int j = 0; j < JN; ++j) {
-      const int m = tile.m0 + (2 * j + hm) * 32 + r;
-      const bool row = m < tile.hi;
-      if constexpr (kMode == kTileGated) {
-        // accumulators 0, 1 are gates, 2, 3 the same outputs' ups
+      for (int j = 0; j < JN; ++j)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int c = 0; c < 4; ++c) {
+          const int i = c >> 1, v = (c & 1) * 8;
+          const int nn = tile.n0 + hn * 64 + i * 32 + v * 2 + h * 8;
+          float g[8], u[8], o[8];
 #pragma unroll
-          for (int v = 0; v < 16; v += 8) {
-            const int nn = tile.n0 + hn * 64 + i * 32 + v * 2 + h * 8;
-            float g[8], u[8], o[8];
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-              g[x] = acc[i][j][v + x];
-              u[x] = acc[i + 2][j][v + x];
-              o[x] = Sigmoid(g[x]).times(g[x]) * u[x];
-            }
-            if (row && nn < p.n) {
-              store8_at<true>(p.y, (size_t)m * p.n + nn, o);
-              if (p.pre) {
-                store8_at<true>(p.pre, (size_t)m * 2 * p.n + nn, g);
-                store8_at<true>(p.pre, (size_t)m * 2 * p.n + p.n + nn, u);
-              }
-            }
-            __builtin_amdgcn_sched_barrier(0);  // a few accumulators at a time: no spills
+          for (int x = 0; x < 8; ++x) g[x] = acc[i][j][v + x], u[x] = acc[i + 2][j][v + x];
+          gated<8>(g, u, o);
+          const int at = (row0 + 64 * j) * pitch + nn * 2;
+          y.store8<true>(nn < p.n ? at : INT32_MIN, o);
+          if (p.pre) {
+            const int pt = at + (row0 + 64 * j) * pitch;
+            pre.store8<true>(nn < p.n ? pt : INT32_MIN, g);
+            pre.store8<true>(nn < p.n ? pt + pitch : INT32_MIN, u);
           }
+          __builtin_amdgcn_sched_barrier(0);  // a few accumulators at a time: no spills
         }
-      } else {
+    } else {
+      const int wide = kGateGrad ? 2 * p.n : p.n, pitch = wide * kElt;
+      const size_t m = (kSum ? (size_t)tile.e * p.k : 0) + tile.m0;
+      uint8_t* const to = static_cast<uint8_t*>(p.y) + m * pitch;
+      const RowBuffer y(to, rows, pitch);
+      const RowBuffer in(kGateGrad ? static_cast<void*>(p.pre + m * wide) : to,
+                         kGateGrad || kAdd ? rows : 0, pitch);
+      auto offset = [&](int j, int c) {
+        const int nn = tile.n0 + hn * 128 + (c >> 1) * 32 + (c & 1) * 16 + h * 8;
+        return nn < p.n ? (row0 + 64 * j) * pitch + nn * kElt : INT32_MIN;
+      };
+      // what a chunk of 8 needs is read 8 chunks before it
+      u32x4 ahead[8][2];
+      auto fetch = [&](int j, int c) {
+        if constexpr (kGateGrad || kAdd) {
+          const int at = offset(j, c);
+          ahead[c][0] = in.load(at);
+          if constexpr (kGateGrad) ahead[c][1] = in.load(at < 0 ? at : at + p.n * 2);
+          if constexpr (kAdd && !kBF16) ahead[c][1] = in.load(at < 0 ? at : at + 16);
+        }
+      };
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+      for (int c = 0; c < 8; ++c) fetch(0, c);
 #pragma unroll
-          for (int v = 0; v < 16; v += 8) {
-            const int nn = tile.n0 + hn * 128 + i * 32 + v * 2 + h * 8;
-            if (kMode == kTileGateGrad || kSum) __builtin_amdgcn_sched_barrier(0);
-            if (!row || nn >= p.n) continue;
-            float o[8];
+      for (int j = 0; j < JN; ++j)
 #pragma unroll
-            for (int x = 0; x < 8; ++x) o[x] = acc[i][j][v + x];
-            if constexpr (kMode == kTileGateGrad) {
-              float g[8], u[8], du[8];
-              load8<true>(p.pre + (size_t)m * 2 * p.n + nn, 0, g);
-              load8<true>(p.pre + (size_t)m * 2 * p.n + p.n + nn, 0, u);
+        for (int c = 0; c < 8; ++c) {
+          const int i = c >> 1, v = (c & 1) * 8, at = offset(j, c);
+          float o[8];
 #pragma unroll
-              for (int x = 0; x < 8; ++x) {
-                const Sigmoid s(g[x]);
-                du[x] = s.times(o[x] * g[x]);
-                o[x] = s.times(o[x] * u[x]) * (1.0f + g[x] * s.rest);
+          for (int x = 0; x < 8; ++x) o[x] = acc[i][j][v + x];
+          if constexpr (kGateGrad) {
+            float g[8], u[8], du[8];
+            bf16_of(ahead[c][0], g);
+            bf16_of(ahead[c][1], u);
+            if (j + 1 < JN) fetch(j + 1, c);
+            gate_grad<8>(g, u, o, du);
+            y.store8<true>(at, o);
+            y.store8<true>(at < 0 ? at : at + p.n * 2, du);
+          } else {
+            if constexpr (kAdd) {
+              float b[8];
+              if constexpr (kBF16) {
+                bf16_of(ahead[c][0], b);
+              } else {
+#pragma unroll
+                for (int x = 0; x < 8; ++x) b[x] = __uint_as_float(ahead[c][x >> 2][x & 3]);
               }
-              store8_at<true>(p.y, (size_t)m * 2 * p.n + nn, o);
-              store8_at<true>(p.y, (size_t)m * 2 * p.n + p.n + nn, du);
-            } else if constexpr (kSum) {
-              const size_t at = ((size_t)tile.e * p.k + m) * p.n + nn;
-              if (p.add) {
-                float b[8];
-                load8<kBF16>(static_cast<char*>(p.y) + at * (kBF16 ? 2 : 4), 0, b);
 #pragma unroll
-                for (int x = 0; x < 8; ++x) o[x] += b[x];
-              }
-              store8_at<kBF16>(p.y, at, o);
-            } else {
-              store8_at<kBF16>(p.y, (size_t)m * p.n + nn, o);
+              for (int x = 0; x < 8; ++x) o[x] += b[x];
+              if (j + 1 < JN) fetch(j + 1, c);
             }
+            y.store8<kBF16>(at, o);
           }
+          if (kGateGrad || kAdd || c == 7) __builtin_amdgcn_sched_barrier(0);
         }
-      }
-      __builtin_amdgcn_sched_barrier(0);  // one row of accumulators at a time: no spills
     }
   };
+  int stored = 0;
   for (int it = 0; it < tiles; ++it) {
-    const BfTile tile = tile_of(tile_index(it));
-    if (kSum || tile.hi - tile.m0 > BM / 2)
-      run(tile, std::false_type());
-    else
-      run(tile, std::true_type());
+    const BfTile tile = c_it == it ? at0 : c_it == it + 1 ? at1 : at2;
+    if (kSum || kLora || tile.hi - tile.m0 > BM / 2) {
+      run(tile, stored, std::false_type());
+      stored = 2;
+    } else {
+      run(tile, stored, std::true_type());
+      stored = 1;
+    }
   }
   // no copy may reach LDS after the workgroup has given it back
   wait_barrier<0>();

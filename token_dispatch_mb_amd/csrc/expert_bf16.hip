@@ -76,20 +76,25 @@ hipError_t launch_expert_bf16_wgrad(const mb_dims& d, const Geometry& g, const m
                                     const uint16_t* dy, const uint16_t* a, void* dw,
                                     hipStream_t st) {
   TileArgs p = plan_args(d, g, o);
-  p.a = dy, p.w = a, p.y = dw, p.n = k_in, p.k = n_out, p.add = add;
-  const dim3 grid(kCus), block(kExpertThreads);
+  p.a = dy, p.w = a, p.y = dw, p.n = k_in, p.k = n_out;
+  // 256 rows to a tile where they occupy the CUs
   const int64_t tiles = (int64_t)p.E * ((p.k + 255) / 256) * ((p.n + kTileN - 1) / kTileN);
+#define MB_W(BF16, JT)                                                                       \
+  do {                                                                                       \
+    if (add)                                                                                 \
+      hipLaunchKernelGGL((k_bf16_tile<kTileWeightAdd, BF16, JT>), grid, block, 0, st, p);    \
+    else                                                                                     \
+      hipLaunchKernelGGL((k_bf16_tile<kTileWeightGrad, BF16, JT>), grid, block, 0, st, p);   \
+  } while (0)
+  const dim3 grid(kCus), block(kExpertThreads);
   if (tiles >= kCus) {
-    if (bf16)
-      hipLaunchKernelGGL((k_bf16_tile<kTileWeightGrad, true, 4>), grid, block, 0, st, p);
-    else
-      hipLaunchKernelGGL((k_bf16_tile<kTileWeightGrad, false, 4>), grid, block, 0, st, p);
+    if (bf16) MB_W(true, 4);
+    else MB_W(false, 4);
   } else {
-    if (bf16)
-      hipLaunchKernelGGL((k_bf16_tile<kTileWeightGrad, true, 2>), grid, block, 0, st, p);
-    else
-      hipLaunchKernelGGL((k_bf16_tile<kTileWeightGrad, false, 2>), grid, block, 0, st, p);
+    if (bf16) MB_W(true, 2);
+    else MB_W(false, 2);
   }
+#undef MB_W
   return hipGetLastError();
 }
 
