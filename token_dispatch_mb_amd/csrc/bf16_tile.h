@@ -480,6 +480,13 @@ __device__ __forceinline__ void bf16_of(u32x4 u, float* v) {
   }
 }
 
+// Waits until this wave's LDS reads are done and at most N of its memory
+// operations, or the 63 that can be counted, are outstanding.
+template <int N>
+__device__ __forceinline__ void wait_stores() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N < 63 ? N : 63) : "memory");
+}
+
 template <int kMode, bool kBF16, int JT>
 __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
   constexpr int BM = 64 * JT, JH = JT / 2;
@@ -657,11 +664,17 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
   // they are issued: kept from stage to stage, the compiler may hold it in
   // vector registers.) last: all ones in a tile's last stage (kRows).
   auto last_stage = [&] { return c_left == 1 ? 0xffffffffu : 0u; };
-  auto copy_w = [&](i32x4 b, uint32_t last, int c) {
+  // Row pitches that the compiler does not know to be the same every time: it
+  // would keep every copy's offset in a register of its own, and spill them.
+  auto fresh = [](int v) {
+    asm volatile("" : "+s"(v));
+    return v;
+  };
+  auto copy_w = [&](i32x4 b, uint32_t last, int pw, int c) {
     copy16(b, (lds_ptr)(lds.w[c_buf] + (wave * 8 + c) * 1024),
            (cw[c & 1] + c * kRowsW * pw) | (kColW ? 0u : cut_w[c & 1] & last), 0);
   };
-  auto copy_a = [&](i32x4 b, uint32_t last, int c) {
+  auto copy_a = [&](i32x4 b, uint32_t last, int pa, int c) {
     copy16(b, (lds_ptr)(lds.a[c_buf] + (wave * 2 * JT + c) * 1024),
            (ca[c & 1] + c * kRowsA * pa) | (kColA ? 0u : cut_a[c & 1] & last), 0);
   };
@@ -717,9 +730,9 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
   for (int s = 0; s < 2; ++s) {
     const i32x4 bw = ow.buffer(pw), ba = oa.buffer(pa);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) copy_w(bw, last_stage(), c);
+    for (int c = 0; c < 8; ++c) copy_w(bw, last_stage(), pw, c);
 #pragma unroll
-    for (int c = 0; c < 2 * JT; ++c) copy_a(ba, last_stage(), c);
+    for (int c = 0; c < 2 * JT; ++c) copy_a(ba, last_stage(), pa, c);
     next_stage();
   }
   wait_barrier<0>();
@@ -729,13 +742,11 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
 #pragma unroll
   for (int t = 0; t < JH; ++t) read_a(0, 0, t, 0), read_a(0, 0, t, 1);
 
-  // A tile of no more than half its rows (a slot's last) leaves the second
-  // half of every wave's accumulators out, the waves' row tiles taking turns.
-  // stored: whether the tile before was whole (2) or half (1); 0 before the
-  // first.
-  auto run = [&](const BfTile& tile, int stored, auto half_) {
-    constexpr bool kHalf = decltype(half_)::value;
-    constexpr int JN = kHalf ? JH : JT;
+  // A tile of fewer rows (a slot's last) leaves out accumulators of every
+  // wave, 64 rows at a time, the waves' row tiles taking turns: JN of JT are
+  // left. stored: JN of the tile before, 0 before the first.
+  auto run = [&](const BfTile& tile, int stored, auto jn_) {
+    constexpr int JN = decltype(jn_)::value, J1 = JN < JH ? JN : JH;
     f32x16 acc[4][JN];
     auto stage = [&](auto first_) {
       constexpr bool kFirst = decltype(first_)::value;
@@ -743,15 +754,16 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
       for (int e = 0; e < 2; ++e) {
         const i32x4 bw = ow.buffer(pw), ba = oa.buffer(pa);
         const uint32_t last = last_stage();
+        const int pitch_w = fresh(pw), pitch_a = fresh(pa);
         // first half: the rows of the second are read under it
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const int u = c >> 2, i = c & 3;
 #pragma unroll
-          for (int j = 0; j < JH; ++j)
+          for (int j = 0; j < J1; ++j)
             acc[i][j] = mfma_bf16(fw[i][u], fa[j][u], kFirst && !e && !u ? f32x16{} : acc[i][j]);
-          if (!kHalf && c < JT) read_a(buf, e, JH + (c >> 1), c & 1);
-          if (e) copy_w(bw, last, c);
+          if (c < 2 * (JN - J1)) read_a(buf, e, JH + (c >> 1), c & 1);
+          if (e) copy_w(bw, last, pitch_w, c);
           __builtin_amdgcn_sched_barrier(0);
         }
         if (e) {
@@ -762,14 +774,16 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
           // under way: at least kStores for each 32 rows, of the 63 that can
           // be counted.
           if constexpr (kFirst) {
-            constexpr int kWhole = JT * kStores + 8 < 63 ? JT * kStores + 8 : 63;
-            constexpr int kPart = JH * kStores + 8 < 63 ? JH * kStores + 8 : 63;
-            if (stored == 2)
-              asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kWhole) : "memory");
-            else if (stored == 1)
-              asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kPart) : "memory");
+            if (JT > 3 && stored > 3)
+              wait_stores<4 * kStores + 8>();
+            else if (JT > 2 && stored > 2)
+              wait_stores<3 * kStores + 8>();
+            else if (stored > 1)
+              wait_stores<2 * kStores + 8>();
+            else if (stored > 0)
+              wait_stores<kStores + 8>();
             else
-              asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)" ::: "memory");
+              wait_stores<8>();
             asm volatile("s_barrier" ::: "memory");
           } else {
             wait_barrier<8>();
@@ -788,7 +802,7 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
           if (c < JT) read_a(buf, 1 - e, c >> 1, c & 1);
           if (e) {
 #pragma unroll
-            for (int d = c * JT / 4; d < (c + 1) * JT / 4; ++d) copy_a(ba, last, d);
+            for (int d = c * JT / 4; d < (c + 1) * JT / 4; ++d) copy_a(ba, last, pitch_a, d);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -799,6 +813,12 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
     const int stages = stages_of(tile.e);
     stage(std::true_type());
     for (int s = 1; s < stages; ++s) stage(std::false_type());
+    // the accumulators are in the matrix unit's registers (nothing runs here:
+    // it keeps the allocator from moving them in and out in the loop)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < JN; ++j) asm volatile("" : "+a"(acc[i][j]));
     if constexpr (kLora) {
       // the reduction goes on over the ranks of every adapter among the
       // wave's rows, with zeros in the rows of the others
@@ -838,10 +858,11 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
     }
     // ---- the outputs: 8 consecutive ones of a row at a time ----
     const int rows = min(tile.hi - tile.m0, BM);
-    const int row0 = hm * 32 + r;  // + 64 j
+    int row0 = hm * 32 + r;  // + 64 j
+    asm volatile("" : "+v"(row0));  // as `fresh`
     if constexpr (kGated) {
       // accumulators 0, 1 are gates, 2, 3 the same outputs' ups
-      const int pitch = p.n * 2;
+      const int pitch = fresh(p.n * 2);
       const RowBuffer y(static_cast<uint16_t*>(p.y) + (size_t)tile.m0 * p.n, rows, pitch);
       const RowBuffer pre(p.pre + (size_t)tile.m0 * 2 * p.n, p.pre ? rows : 0, 2 * pitch);
 #pragma unroll
@@ -864,7 +885,8 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
           __builtin_amdgcn_sched_barrier(0);  // a few accumulators at a time: no spills
         }
     } else {
-      const int wide = kGateGrad ? 2 * p.n : p.n, pitch = wide * kElt;
+      const int wide = kGateGrad ? 2 * p.n : p.n;
+      const int pitch = fresh(wide * kElt);
       const size_t m = (kSum ? (size_t)tile.e * p.k : 0) + tile.m0;
       uint8_t* const to = static_cast<uint8_t*>(p.y) + m * pitch;
       const RowBuffer y(to, rows, pitch);
@@ -924,13 +946,20 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
   int stored = 0;
   for (int it = 0; it < tiles; ++it) {
     const BfTile tile = c_it == it ? at0 : c_it == it + 1 ? at1 : at2;
-    if (kSum || kLora || tile.hi - tile.m0 > BM / 2) {
-      run(tile, stored, std::false_type());
-      stored = 2;
-    } else {
-      run(tile, stored, std::true_type());
-      stored = 1;
+    // (outputs of sums over an expert's rows, and of one long batch, have one
+    // such tile in a column)
+    const int jn = kSum || kLora ? JT : min((tile.hi - tile.m0 + 63) / 64, JT);
+    if (jn == JT)
+      run(tile, stored, std::integral_constant<int, JT>());
+    else if constexpr (!kSum && !kLora) {
+      if (JT > 3 && jn == 3)
+        run(tile, stored, std::integral_constant<int, (JT > 3 ? 3 : 1)>());
+      else if (JT > 2 && jn == 2)
+        run(tile, stored, std::integral_constant<int, (JT > 2 ? 2 : 1)>());
+      else
+        run(tile, stored, std::integral_constant<int, 1>());
     }
+    stored = jn;
   }
   // no copy may reach LDS after the workgroup has given it back
   wait_barrier<0>();
