@@ -8,12 +8,13 @@
 // lane % 32 of the product is row r of the tile, and with h = lane / 32, rows
 // 8a + 4h + b of the product are at accumulator 4a + b.
 //
-// A stage takes 64 elements of the reduction. Its operands are copied from
-// memory into LDS without passing registers, 64 KB (JT = 4) in two buffers:
-// the stage two ahead is copied over the present one, the columns once all of
-// these are in registers, the rows half a step later. The stages of a
-// workgroup's tiles form one sequence, so that a tile's first copies run
-// under the end of the tile before it.
+// A stage takes 64 elements of the reduction, in two steps of 32. Its operands
+// are copied from memory into LDS without passing registers, 64 KB (JT = 4) in
+// two buffers, and read from there into registers a step before their
+// products. That empties a buffer's columns a quarter into step 0, and its rows
+// at its end: the stage two ahead is copied there under the rest of step 0 and
+// under step 1. The stages of a workgroup's tiles form one sequence, so that a
+// tile's first copies run under the end of the tile before it.
 //
 // An operand comes in one of two layouts:
 //  * kRows: its rows are contiguous along the reduction (weights in the
@@ -183,6 +184,8 @@ __device__ __forceinline__ i32x4 read_tr(const uint8_t* lo, const uint8_t* hi) {
   return i32x4{a[0], a[1], b[0], b[1]};
 }
 
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 // What the copies of one operand read in a stage. kRows: `left` bytes from
 // `at`. kCols: of `left` reduction rows those that a wave copies, from column
 // `col` on. Nothing where left is 0 or less.
@@ -192,7 +195,8 @@ struct Operand {
   int left, col;
 
   __device__ __forceinline__ i32x4 buffer(int pitch) const {
-    return buffer_of(at, kCols ? max(min(max(left, 0), 16) * pitch - col * 2, 0) : max(left, 0));
+    return buffer_of(at, kCols ? max(uniform(min(max(left, 0), 16)) * pitch - col * 2, 0)
+                               : max(left, 0));
   }
   __device__ __forceinline__ void next(int pitch) {
     at += kCols ? 32 * (int64_t)pitch : 64;
@@ -224,7 +228,6 @@ struct ExpertLists {
   int16_t first[kMaxExperts];    // its first, -1: none
 };
 
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 template <int BM, class Args>
 __device__ void slot_table(const Args& p, int nslots, SlotTable& t, int* part) {
@@ -458,19 +461,26 @@ struct RowBuffer {
   __device__ __forceinline__ u32x4 load(int off) const {
     return __builtin_amdgcn_raw_buffer_load_b128(at, off, 0, 0);
   }
-  template <bool kBF16>
-  __device__ __forceinline__ void store8(int off, const float* v) const {
-    if constexpr (kBF16) {
-      store(off, u32x4{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]),
-                       bf16x2_rne(v[6], v[7])});
-    } else {
-      store(off, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                       __float_as_uint(v[3])});
-      store(off + 16, u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
-                            __float_as_uint(v[7])});
-    }
-  }
 };
+
+// Exchanges the odd rows of 16 lanes of a with the even ones of b. Where a
+// lane (r = lane % 32, h = lane / 32) has two 16-byte pieces of row r of an
+// output, this leaves one of rows 0 to 15 and one of rows 16 to 31, such that
+// four lanes hold 64 consecutive bytes: whole requests to memory. It undoes
+// itself.
+__device__ __forceinline__ void swap16(u32x4& a, u32x4& b) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const auto v = __builtin_amdgcn_permlane16_swap(a[i], b[i], false, false);
+    a[i] = v[0];
+    b[i] = v[1];
+  }
+}
+
+__device__ __forceinline__ u32x4 bf16x8_rne(const float* v) {
+  return u32x4{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]),
+               bf16x2_rne(v[6], v[7])};
+}
 
 __device__ __forceinline__ void bf16_of(u32x4 u, float* v) {
 #pragma unroll
@@ -489,7 +499,7 @@ __device__ __forceinline__ void wait_stores() {
 
 template <int kMode, bool kBF16, int JT>
 __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
-  constexpr int BM = 64 * JT, JH = JT / 2;
+  constexpr int BM = 64 * JT;
   constexpr bool kLora = kMode == kTileLora, kGated = kMode == kTileGated;
   constexpr bool kGateGrad = kMode == kTileGateGrad, kAdd = kMode == kTileWeightAdd;
   constexpr bool kSum = kMode == kTileWeightGrad || kAdd;
@@ -596,15 +606,16 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
     }
   }
   constexpr int kRowsW = kColW ? 2 : 8, kRowsA = kColA ? 64 / kPiecesA : 8;  // of a copy
-  // Place of the copies in the sequence of stages: two ahead of the product.
+  // Place of the copies in the sequence of stages: one ahead of the products,
+  // two from the first quarter of a stage on.
   // A wave copies a quarter of each operand. Past the last tile the buffers
   // are empty: zeros, unused.
   Operand<kColW> ow;
   Operand<kColA> oa;
   int c_it = 0, c_left = 0, c_buf = 0, c_slot = 0, c_n0 = 0, c_m0 = 0;
-  // the tile that the copies are at, and the two before it: the product's is
-  // among them
-  BfTile at0 = {}, at1 = {}, at2 = {};
+  // the tile that the copies are at, and the one before it: when the products
+  // come to a tile, the copies are at its second stage or at the next tile
+  BfTile at0 = {}, at1 = {};
   // kSum: the rows of slot j, none where it is negative
   auto sum_slot = [&](int j) {
     if constexpr (kSum) {
@@ -617,7 +628,6 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
   };
   auto aim = [&](int it) {
     const BfTile t = tile_of(tile_index(it));
-    at2 = at1;
     at1 = at0;
     at0 = t;
     c_left = stages_of(t.e);
@@ -626,22 +636,24 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
       c_m0 = t.m0;
       sum_slot(uniform(table.first[t.e]));
     } else {
-      const int m = t.m0 + wave * 16 * JT, nm = min(max(t.hi - m, 0), 16 * JT);
+      const int m = t.m0 + wave * 16 * JT, nm = uniform(min(max(t.hi - m, 0), 16 * JT));
       oa = {p.a + (int64_t)m * p.k, nm * pa, 0};
       if constexpr (kColW) {  // reduction rows, each wave its 16 of a stage
         ow = {p.w + ((int64_t)t.e * p.k + wave * 16) * p.n + t.n0, p.k - wave * 16, t.n0};
       } else if constexpr (kGated) {
         // waves 0 and 2 copy gate rows, 1 and 3 the up rows of the same outputs
-        const int n = t.n0 + (wave >> 1) * 64, nn = min(max(p.n - n, 0), 64);
+        const int n = t.n0 + (wave >> 1) * 64, nn = uniform(min(max(p.n - n, 0), 64));
         ow = {p.w + (((int64_t)t.e * 2 + (wave & 1)) * p.n + n) * p.k, nn * pw, 0};
       } else {
-        const int n = t.n0 + wave * 64, nn = min(max(p.n - n, 0), 64);
+        const int n = t.n0 + wave * 64, nn = uniform(min(max(p.n - n, 0), 64));
         ow = {p.w + ((int64_t)t.e * p.n + n) * p.k, nn * pw, 0};
       }
     }
   };
   auto next_stage = [&] {
     c_buf ^= 1;
+    ow.next(pw);
+    oa.next(pa);
     if (--c_left == 0) {
       ++c_it;
       if (c_it < tiles) {
@@ -650,42 +662,58 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
       }
       ow.left = oa.left = 0;
       c_left = 1 << 30;
-      at2 = at1;
       at1 = at0;
-    } else {
-      ow.next(pw);
-      oa.next(pa);
-      if constexpr (kSum) {
-        if (c_it < tiles && ow.left + wave * 16 <= 0) sum_slot(uniform(table.next[c_slot]));
-      }
+    } else if constexpr (kSum) {
+      if (__builtin_expect(c_it < tiles && ow.left + wave * 16 <= 0, 0))
+        sum_slot(uniform(table.next[c_slot]));
     }
   };
-  // A stage's copies from buffer b. (The buffer is put together just before
-  // they are issued: kept from stage to stage, the compiler may hold it in
-  // vector registers.) last: all ones in a tile's last stage (kRows).
-  auto last_stage = [&] { return c_left == 1 ? 0xffffffffu : 0u; };
-  // Row pitches that the compiler does not know to be the same every time: it
-  // would keep every copy's offset in a register of its own, and spill them.
+  // A pitch that the compiler does not know to be the same every time: it
+  // would keep offsets that follow from it in registers of their own, and
+  // spill them.
   auto fresh = [](int v) {
     asm volatile("" : "+s"(v));
     return v;
   };
-  auto copy_w = [&](i32x4 b, uint32_t last, int pw, int c) {
-    copy16(b, (lds_ptr)(lds.w[c_buf] + (wave * 8 + c) * 1024),
-           (cw[c & 1] + c * kRowsW * pw) | (kColW ? 0u : cut_w[c & 1] & last), 0);
+  // A stage's copies. (The buffers are put together in every stage: kept from
+  // stage to stage, the compiler may hold them in vector registers.) The
+  // copies of one operand are issued in order, each moving its lanes' offsets
+  // on: between two products there is room for seven instructions.
+  struct Copies {
+    i32x4 buf;
+    uint32_t at[2];
+    int step;
   };
-  auto copy_a = [&](i32x4 b, uint32_t last, int pa, int c) {
-    copy16(b, (lds_ptr)(lds.a[c_buf] + (wave * 2 * JT + c) * 1024),
-           (ca[c & 1] + c * kRowsA * pa) | (kColA ? 0u : cut_a[c & 1] & last), 0);
+  auto last_stage = [&] { return c_left == 1 ? 0xffffffffu : 0u; };  // of a tile
+  auto offsets_w = [&](Copies& c) {
+    const int pitch = fresh(pw);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      c.at[j] = (cw[j] + j * kRowsW * pitch) | (kColW ? 0u : cut_w[j] & last_stage());
+    c.step = 2 * kRowsW * pitch;
+  };
+  auto offsets_a = [&](Copies& c) {
+    const int pitch = fresh(pa);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      c.at[j] = (ca[j] + j * kRowsA * pitch) | (kColA ? 0u : cut_a[j] & last_stage());
+    c.step = 2 * kRowsA * pitch;
+  };
+  auto copy_w = [&](Copies& c, int y) {
+    copy16<0>(c.buf, (lds_ptr)(lds.w[c_buf] + (wave * 8 + y) * 1024), c.at[y & 1], 0);
+    c.at[y & 1] += c.step;
+  };
+  auto copy_a = [&](Copies& c, int y) {
+    copy16<0>(c.buf, (lds_ptr)(lds.a[c_buf] + (wave * 2 * JT + y) * 1024), c.at[y & 1], 0);
+    c.at[y & 1] += c.step;
   };
 
-  // ---- operands of the matrix unit, [accumulator][product of the step] ----
-  // Each register is read from LDS for the next step as soon as its last
-  // product of this one is issued: the rows in two halves, the columns along
-  // the second half. Column n of a wave's 32 enters the matrix unit as row
-  // swap23(n), bits 2 and 3 exchanged, which leaves a lane 8 consecutive
-  // outputs in 8 consecutive accumulators.
-  i32x4 fw[4][2], fa[JT][2];
+  // ---- operands of the matrix unit, [step][accumulator][product] ----
+  // A step's are read from LDS under the products of the step before. Column n
+  // of a wave's 32 enters the matrix unit as row swap23(n), bits 2 and 3
+  // exchanged, which leaves a lane 8 consecutive outputs in 8 consecutive
+  // accumulators.
+  i32x4 fw[2][4][2], fa[2][JT][2];
   constexpr int kPitchW = kTileN * 2, kPitchA = BM * 2;  // of reduction rows (kCols)
   const int piece = ((2 * h) ^ ((r >> 1) & 7)) << 4;     // kRows: of (step 0, h, 0)
   const int swapped = (r & 19) | ((r & 4) << 1) | ((r & 8) >> 1);
@@ -711,104 +739,128 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
   auto read_w = [&](int buf, int step, int t, int u) {
     if constexpr (kColW) {
       const uint8_t* s = lds.w[buf] + at_w[t] + (step * 32 + u * 8) * kPitchW;
-      fw[t][u] = read_tr(s, s + 4 * kPitchW);
+      fw[step][t][u] = read_tr(s, s + 4 * kPitchW);
     } else {
-      fw[t][u] = load16(lds.w[buf] + at_w[t] + (piece ^ (step * 64 + u * 16)));
+      fw[step][t][u] = load16(lds.w[buf] + at_w[t] + (piece ^ (step * 64 + u * 16)));
     }
   };
   auto read_a = [&](int buf, int step, int t, int u) {
     if constexpr (kColA) {
       const uint8_t* s = lds.a[buf] + at_a[t] + (step * 32 + u * 8) * kPitchA;
-      fa[t][u] = read_tr(s, s + 4 * kPitchA);
+      fa[step][t][u] = read_tr(s, s + 4 * kPitchA);
     } else {
-      fa[t][u] = load16(lds.a[buf] + at_a[t] + (piece ^ (step * 64 + u * 16)));
+      fa[step][t][u] = load16(lds.a[buf] + at_a[t] + (piece ^ (step * 64 + u * 16)));
     }
+  };
+  // What step 1 reads for the next stage, y of kNext: all operands of its step
+  // 0, in the order in which the products need them (of each u, column 0, the
+  // rows, columns 1 to 3), then the columns of its step 1's first products.
+  constexpr int kNext = 2 * (4 + JT) + 4;
+  auto read_next = [&](int buf, int y) {
+    const int u = y / (4 + JT), i = y % (4 + JT);
+    if (u > 1)
+      read_w(buf, 1, i, 0);
+    else if (i == 0)
+      read_w(buf, 0, 0, u);
+    else if (i <= JT)
+      read_a(buf, 0, i - 1, u);
+    else
+      read_w(buf, 0, i - JT, u);
   };
 
   aim(0);
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    const i32x4 bw = ow.buffer(pw), ba = oa.buffer(pa);
+    if (s) next_stage();
+    Copies to_w = {settled(ow.buffer(pw))}, to_a = {settled(oa.buffer(pa))};
+    offsets_w(to_w);
+    offsets_a(to_a);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) copy_w(bw, last_stage(), pw, c);
+    for (int y = 0; y < 8; ++y) copy_w(to_w, y);
 #pragma unroll
-    for (int c = 0; c < 2 * JT; ++c) copy_a(ba, last_stage(), pa, c);
-    next_stage();
+    for (int y = 0; y < 2 * JT; ++y) copy_a(to_a, y);
   }
   wait_barrier<0>();
   int buf = 0;
 #pragma unroll
-  for (int t = 0; t < 4; ++t) read_w(0, 0, t, 0), read_w(0, 0, t, 1);
-#pragma unroll
-  for (int t = 0; t < JH; ++t) read_a(0, 0, t, 0), read_a(0, 0, t, 1);
+  for (int y = 0; y < kNext; ++y) read_next(0, y);
 
   // A tile of fewer rows (a slot's last) leaves out accumulators of every
   // wave, 64 rows at a time, the waves' row tiles taking turns: JN of JT are
   // left. stored: JN of the tile before, 0 before the first.
   auto run = [&](const BfTile& tile, int stored, auto jn_) {
-    constexpr int JN = decltype(jn_)::value, J1 = JN < JH ? JN : JH;
+    constexpr int JN = decltype(jn_)::value;
     f32x16 acc[4][JN];
+    // Under the products of a stage: the rest of its own operands (step 0),
+    // those that read_next names of the next (step 1), and the copies of the
+    // stage two ahead, the columns' from the moment when all waves have read
+    // the present ones (step 0), the rows' in step 1. A product takes 32 cycles,
+    // a wave issues in order, and there is one wave to a SIMD: what stands
+    // between two products beyond those cycles leaves the matrix unit idle, so
+    // no more than a few instructions do, and the copies (16 cycles each of
+    // the address unit that the four waves share) are spread evenly.
     auto stage = [&](auto first_) {
       constexpr bool kFirst = decltype(first_)::value;
+      constexpr int kProducts = 8 * JN;  // of a step
+      constexpr int kRead = 3 * JN;  // from here on the stage's columns are copied over
+      Copies to_w, to_a;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const i32x4 bw = ow.buffer(pw), ba = oa.buffer(pa);
-        const uint32_t last = last_stage();
-        const int pitch_w = fresh(pw), pitch_a = fresh(pa);
-        // first half: the rows of the second are read under it
+      for (int x = 0; x < kProducts; ++x) {
+        const int c = x / JN, j = x % JN, u = c >> 2, i = c & 3;
+        // all columns of the stage are in this wave's registers; after the
+        // barrier, in every wave's
+        if (x == kRead) read_barrier();
+        // where the copies of the stage two ahead read
+        if (x == JN) next_stage();
+        if (x == 2 * JN) to_w.buf = settled(ow.buffer(pw));
+        if (x == 2 * JN + 1) offsets_w(to_w);
+        if (x == 5 * JN) to_a.buf = settled(oa.buffer(pa));
+        if (x == 5 * JN + 1) offsets_a(to_a);
+        acc[i][j] = mfma_bf16(fw[0][i][u], fa[0][j][u], kFirst && !u ? f32x16{} : acc[i][j]);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const int u = c >> 2, i = c & 3;
+        for (int y = 0; y < 4; ++y)
+          if (y * JN / 2 == x) read_w(buf, 1, y, 1);
 #pragma unroll
-          for (int j = 0; j < J1; ++j)
-            acc[i][j] = mfma_bf16(fw[i][u], fa[j][u], kFirst && !e && !u ? f32x16{} : acc[i][j]);
-          if (c < 2 * (JN - J1)) read_a(buf, e, JH + (c >> 1), c & 1);
-          if (e) copy_w(bw, last, pitch_w, c);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        if (e) {
-          // this wave has read all of the stage, and its copies of the next
-          // have landed (the eight just issued are of the one after); after
-          // the barrier that holds for all waves. In a tile's first stage the
-          // stores of the tile before lie between the two, and may still be
-          // under way: at least kStores for each 32 rows, of the 63 that can
-          // be counted.
-          if constexpr (kFirst) {
-            if (JT > 3 && stored > 3)
-              wait_stores<4 * kStores + 8>();
-            else if (JT > 2 && stored > 2)
-              wait_stores<3 * kStores + 8>();
-            else if (stored > 1)
-              wait_stores<2 * kStores + 8>();
-            else if (stored > 0)
-              wait_stores<kStores + 8>();
-            else
-              wait_stores<8>();
-            asm volatile("s_barrier" ::: "memory");
-          } else {
-            wait_barrier<8>();
-          }
-          buf ^= 1;
-        }
-        // second half: the next step's operands are read under it, and the
-        // stage two ahead copied into the buffer just read
+        for (int y = 0; y < 2 * JN; ++y)
+          if (3 * JN + y * 15 / 8 == x) read_a(buf, 1, y % JN, y / JN);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const int u = c >> 2, i = c & 3;
-#pragma unroll
-          for (int j = JH; j < JN; ++j)
-            acc[i][j] = mfma_bf16(fw[i][u], fa[j][u], kFirst && !e && !u ? f32x16{} : acc[i][j]);
-          read_w(buf, 1 - e, i, u);
-          if (c < JT) read_a(buf, 1 - e, c >> 1, c & 1);
-          if (e) {
-#pragma unroll
-            for (int d = c * JT / 4; d < (c + 1) * JT / 4; ++d) copy_a(ba, last, pitch_a, d);
-          }
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        if (!e) read_barrier();  // all columns of the stage are in registers
+        for (int y = 0; y < 8; ++y)
+          if (kRead + y * (kProducts - kRead) / 8 == x) copy_w(to_w, y);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      next_stage();
+      // this wave has read all of the stage, and its copies of the next have
+      // landed (the eight just issued are of the one after); after the barrier
+      // that holds for all waves. In a tile's first stage the stores of the tile
+      // before lie between the two, kStores at least for each 32 rows, and may
+      // still be under way.
+      if constexpr (kFirst) {
+        if (JT > 3 && stored > 3)
+          wait_stores<4 * kStores + 8>();
+        else if (JT > 2 && stored > 2)
+          wait_stores<3 * kStores + 8>();
+        else if (stored > 1)
+          wait_stores<2 * kStores + 8>();
+        else if (stored > 0)
+          wait_stores<kStores + 8>();
+        else
+          wait_stores<8>();
+        asm volatile("s_barrier" ::: "memory");
+      } else {
+        wait_barrier<8>();
+      }
+#pragma unroll
+      for (int x = 0; x < kProducts; ++x) {
+        const int c = x / JN, j = x % JN, u = c >> 2, i = c & 3;
+        acc[i][j] = mfma_bf16(fw[1][i][u], fa[1][j][u], acc[i][j]);
+#pragma unroll
+        for (int y = 0; y < kNext; ++y)
+          if (y * kProducts / kNext == x) read_next(buf ^ 1, y);
+#pragma unroll
+        for (int y = 0; y < 2 * JT; ++y)
+          if (y * kProducts / (2 * JT) == x) copy_a(to_a, y);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      buf ^= 1;
     };
     const int stages = stages_of(tile.e);
     stage(std::true_type());
@@ -856,10 +908,23 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
         }
       }
     }
-    // ---- the outputs: 8 consecutive ones of a row at a time ----
+    // ---- the outputs ----
+    // A lane's pieces of 64 bytes of 32 rows, a and b, to the rows from
+    // 32 (2 j + hm) on (see swap16): `col` is where the 64 bytes begin in the
+    // row, `end` where the row's valid ones end.
     const int rows = min(tile.hi - tile.m0, BM);
-    int row0 = hm * 32 + r;  // + 64 j
-    asm volatile("" : "+v"(row0));  // as `fresh`
+    int row0 = hm * 32 + (lane & 15);  // + 64 j
+    asm volatile("" : "+v"(row0));     // as `fresh`
+    // h's pieces are next to each other in bf16 rows, a and b in fp32 rows
+    const int byte = (lane >> 5) * (kBF16 ? 16 : 32) + ((lane >> 4) & 1) * (kBF16 ? 32 : 16);
+    auto place = [&](int j, int pitch, int col, int end) {
+      return col + byte < end ? (row0 + 64 * j) * pitch + col + byte : INT32_MIN;
+    };
+    auto put = [&](const RowBuffer& to, int at, int pitch, u32x4 a, u32x4 b) {
+      swap16(a, b);
+      to.store(at, a);
+      to.store(at < 0 ? at : at + 16 * pitch, b);
+    };
     if constexpr (kGated) {
       // accumulators 0, 1 are gates, 2, 3 the same outputs' ups
       const int pitch = fresh(p.n * 2);
@@ -868,84 +933,107 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
 #pragma unroll
       for (int j = 0; j < JN; ++j)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int i = c >> 1, v = (c & 1) * 8;
-          const int nn = tile.n0 + hn * 64 + i * 32 + v * 2 + h * 8;
-          float g[8], u[8], o[8];
+        for (int i = 0; i < 2; ++i) {
+          u32x4 g2[2], u2[2], o2[2];
 #pragma unroll
-          for (int x = 0; x < 8; ++x) g[x] = acc[i][j][v + x], u[x] = acc[i + 2][j][v + x];
-          gated<8>(g, u, o);
-          const int at = (row0 + 64 * j) * pitch + nn * 2;
-          y.store8<true>(nn < p.n ? at : INT32_MIN, o);
+          for (int v = 0; v < 2; ++v) {
+            float g[8], u[8], o[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              g[x] = acc[i][j][8 * v + x], u[x] = acc[i + 2][j][8 * v + x];
+            gated<8>(g, u, o);
+            g2[v] = bf16x8_rne(g);
+            u2[v] = bf16x8_rne(u);
+            o2[v] = bf16x8_rne(o);
+          }
+          const int col = (tile.n0 + hn * 64 + i * 32) * 2;
+          put(y, place(j, pitch, col, pitch), pitch, o2[0], o2[1]);
           if (p.pre) {
-            const int pt = at + (row0 + 64 * j) * pitch;
-            pre.store8<true>(nn < p.n ? pt : INT32_MIN, g);
-            pre.store8<true>(nn < p.n ? pt + pitch : INT32_MIN, u);
+            const int at = place(j, 2 * pitch, col, pitch);
+            put(pre, at, 2 * pitch, g2[0], g2[1]);
+            put(pre, at < 0 ? at : at + pitch, 2 * pitch, u2[0], u2[1]);
           }
           __builtin_amdgcn_sched_barrier(0);  // a few accumulators at a time: no spills
         }
     } else {
       const int wide = kGateGrad ? 2 * p.n : p.n;
-      const int pitch = fresh(wide * kElt);
+      const int pitch = fresh(wide * kElt), half = fresh(p.n * 2), end = kGateGrad ? half : pitch;
       const size_t m = (kSum ? (size_t)tile.e * p.k : 0) + tile.m0;
       uint8_t* const to = static_cast<uint8_t*>(p.y) + m * pitch;
       const RowBuffer y(to, rows, pitch);
       const RowBuffer in(kGateGrad ? static_cast<void*>(p.pre + m * wide) : to,
                          kGateGrad || kAdd ? rows : 0, pitch);
-      auto offset = [&](int j, int c) {
-        const int nn = tile.n0 + hn * 128 + (c >> 1) * 32 + (c & 1) * 16 + h * 8;
-        return nn < p.n ? (row0 + 64 * j) * pitch + nn * kElt : INT32_MIN;
+      // 64 bytes at a time: 32 bf16 of an accumulator, or half as many fp32
+      constexpr int kPieces = 4 * kElt / 2;
+      auto where = [&](int j, int c) {
+        return place(j, pitch, (tile.n0 + hn * 128) * kElt + c * 64, end);
       };
-      // what a chunk of 8 needs is read 8 chunks before it
-      u32x4 ahead[8][2];
+      // what a piece needs is read kPieces pieces before it
+      u32x4 ahead[kPieces][kGateGrad ? 4 : 2];
       auto fetch = [&](int j, int c) {
         if constexpr (kGateGrad || kAdd) {
-          const int at = offset(j, c);
-          ahead[c][0] = in.load(at);
-          if constexpr (kGateGrad) ahead[c][1] = in.load(at < 0 ? at : at + p.n * 2);
-          if constexpr (kAdd && !kBF16) ahead[c][1] = in.load(at < 0 ? at : at + 16);
+          const int at = where(j, c);
+#pragma unroll
+          for (int q = 0; q < (kGateGrad ? 4 : 2); ++q)
+            ahead[c][q] = in.load(at < 0 ? at : at + (q & 1) * 16 * pitch + (q >> 1) * half);
         }
       };
 #pragma unroll
-      for (int c = 0; c < 8; ++c) fetch(0, c);
+      for (int c = 0; c < kPieces; ++c) fetch(0, c);
 #pragma unroll
       for (int j = 0; j < JN; ++j)
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const int i = c >> 1, v = (c & 1) * 8, at = offset(j, c);
-          float o[8];
-#pragma unroll
-          for (int x = 0; x < 8; ++x) o[x] = acc[i][j][v + x];
+        for (int c = 0; c < kPieces; ++c) {
+          const int at = where(j, c);
           if constexpr (kGateGrad) {
-            float g[8], u[8], du[8];
-            bf16_of(ahead[c][0], g);
-            bf16_of(ahead[c][1], u);
+            swap16(ahead[c][0], ahead[c][1]);
+            swap16(ahead[c][2], ahead[c][3]);
+            u32x4 dg[2], du[2];
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              float g[8], u[8], d[8], e[8];
+              bf16_of(ahead[c][v], g);
+              bf16_of(ahead[c][2 + v], u);
+#pragma unroll
+              for (int x = 0; x < 8; ++x) d[x] = acc[c][j][8 * v + x];
+              gate_grad<8>(g, u, d, e);
+              dg[v] = bf16x8_rne(d);
+              du[v] = bf16x8_rne(e);
+            }
             if (j + 1 < JN) fetch(j + 1, c);
-            gate_grad<8>(g, u, o, du);
-            y.store8<true>(at, o);
-            y.store8<true>(at < 0 ? at : at + p.n * 2, du);
+            put(y, at, pitch, dg[0], dg[1]);
+            put(y, at < 0 ? at : at + half, pitch, du[0], du[1]);
           } else {
-            if constexpr (kAdd) {
-              float b[8];
+            if constexpr (kAdd) swap16(ahead[c][0], ahead[c][1]);
+            u32x4 o2[2];
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
               if constexpr (kBF16) {
-                bf16_of(ahead[c][0], b);
+                float o[8], b[8] = {};
+                if constexpr (kAdd) bf16_of(ahead[c][v], b);
+#pragma unroll
+                for (int x = 0; x < 8; ++x) o[x] = kAdd ? acc[c][j][8 * v + x] + b[x] : acc[c][j][8 * v + x];
+                o2[v] = bf16x8_rne(o);
               } else {
 #pragma unroll
-                for (int x = 0; x < 8; ++x) b[x] = __uint_as_float(ahead[c][x >> 2][x & 3]);
+                for (int x = 0; x < 4; ++x) {
+                  float o = acc[c >> 1][j][(c & 1) * 8 + 4 * v + x];
+                  if constexpr (kAdd) o += __uint_as_float(ahead[c][v][x]);
+                  o2[v][x] = __float_as_uint(o);
+                }
               }
-#pragma unroll
-              for (int x = 0; x < 8; ++x) o[x] += b[x];
-              if (j + 1 < JN) fetch(j + 1, c);
             }
-            y.store8<kBF16>(at, o);
+            if constexpr (kAdd)
+              if (j + 1 < JN) fetch(j + 1, c);
+            put(y, at, pitch, o2[0], o2[1]);
           }
-          if (kGateGrad || kAdd || c == 7) __builtin_amdgcn_sched_barrier(0);
+          if (kGateGrad || kAdd || c == kPieces - 1) __builtin_amdgcn_sched_barrier(0);
         }
     }
   };
   int stored = 0;
   for (int it = 0; it < tiles; ++it) {
-    const BfTile tile = c_it == it ? at0 : c_it == it + 1 ? at1 : at2;
+    const BfTile tile = c_it == it ? at0 : at1;
     // (outputs of sums over an expert's rows, and of one long batch, have one
     // such tile in a column)
     const int jn = kSum || kLora ? JT : min((tile.hi - tile.m0 + 63) / 64, JT);

@@ -104,17 +104,26 @@ __device__ __forceinline__ i32x4 buffer_of(const void* p, uint32_t bytes) {
 }
 
 // Copies 64 lanes' 16 bytes at buf[voff + soff] to consecutive places of LDS
-// from `to` (wave-uniform; the instruction takes it from m0). No register is
-// written. In assembly because the compiler, for its builtin, waits for every
-// copy in flight before the next read of any LDS; the waits that order copies
-// and reads are wait_barrier's. The compiler does not look into the assembly
-// for hazards: a scalar register that a vector instruction wrote (a lane read
-// back, of a value or a spilled register) is valid for memory instructions
-// five wait states later, m0 after one.
+// from `to` (wave-uniform; the instruction takes it from m0, one instruction
+// after m0 was written). No register is written. In assembly because the
+// compiler, for its builtin, waits for every copy in flight before the next
+// read of any LDS; the waits that order copies and reads are wait_barrier's.
+// The compiler does not look into the assembly for hazards: a scalar register
+// that a vector instruction wrote (a lane read back, of a value or of a
+// spilled register) is valid for memory instructions five wait states later.
+// kNops waits that long before the copy.
+template <int kNops = 4>
 __device__ __forceinline__ void copy16(i32x4 buf, lds_ptr to, uint32_t voff, uint32_t soff) {
-  asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-               ::"{m0}"((uint32_t)(uintptr_t)to), "v"(voff), "s"(buf), "s"(soff)
+  asm volatile("s_nop %4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               ::"{m0}"((uint32_t)(uintptr_t)to), "v"(voff), "s"(buf), "s"(soff), "n"(kNops)
                : "memory");
+}
+
+// For copies without that wait (copy16<0>): a buffer that has waited. Their
+// kernels must not spill scalar registers.
+__device__ __forceinline__ i32x4 settled(i32x4 buf) {
+  asm volatile("s_nop 4" : "+s"(buf));
+  return buf;
 }
 
 }  // namespace mb
