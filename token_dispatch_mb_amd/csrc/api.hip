@@ -614,8 +614,8 @@ static bool lora_ok(const mb_lora_params* p) {
 
 size_t mb_lora_workspace_bytes(const mb_lora_params* prm) {
   if (!lora_ok(prm)) return 0;
-  const size_t v = (size_t)lora_parts(*prm) * prm->n_rows * prm->rank * sizeof(float);
-  return align256(v ? v : 1);
+  const size_t bytes = lora_workspace_floats(*prm) * sizeof(float);
+  return align256(bytes ? bytes : 1);
 }
 
 int mb_project_lora(const mb_lora_params* prm, const uint16_t* x_dev, const uint16_t* w_dev,

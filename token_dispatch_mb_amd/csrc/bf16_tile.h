@@ -56,7 +56,8 @@ enum TileMode {
   kTileGateGrad,  // the same, times the activation's derivatives at pre[p]
   kTileWeightGrad, // y[e] = sum over e's rows of a[p]^T w[p]
   kTileWeightAdd,  // the same, added to y
-  kTileLora       // y[t] = a[t] w^T + v[t] b[adapter[t]]^T
+  kTileLora,      // y[t] = a[t] w^T + v[t] b[adapter[t]]^T
+  kTileSplit      // y[part][t] = a[t] w^T over a part of the reduction
 };
 
 struct TileArgs {
@@ -70,11 +71,12 @@ struct TileArgs {
   int P, E, Eh, NS, R, cap;
   int n;  // columns of the output
   int k;  // length of the reduction; weights' gradient: rows of the output
-  // kTileLora: one slot of `cap` rows
+  // kTileLora, kTileSplit: one slot of `cap` rows
   const float* v;          // [parts][cap][rank], whose sum over the parts counts
   const uint16_t* b;       // [L][n][rank]
   const int32_t* adapter;  // [cap]
   int rank, L, parts;
+  int splits, split_stages;  // kTileSplit: parts, and stages (64 elements) of one
 };
 
 // The adapter of a row; none (INT32_MAX) where its number is not one.
@@ -105,6 +107,31 @@ __device__ __forceinline__ void load_v(const TileArgs& p, int row, int at, bool 
       s[2 * x] = fabsf(s[2 * x]) < INFINITY ? s[2 * x] - __uint_as_float(a) : 0.0f;
       s[2 * x + 1] = fabsf(s[2 * x + 1]) < INFINITY ? s[2 * x + 1] - __uint_as_float(b) : 0.0f;
     }
+}
+
+// o[0..4) += outputs [n, n + 4) of a row's adapter. A lane by itself: rows may
+// have different adapters, and an output's ranks are consecutive in memory.
+__device__ __forceinline__ void add_adapter(const TileArgs& p, int row, int n, float* o) {
+  const int id = adapter_of(p, row);
+  if (id == INT32_MAX) return;
+  const uint16_t* b = p.b + ((size_t)id * p.n + n) * p.rank;
+#pragma unroll 2
+  for (int q = 0; q < p.rank; q += 8) {
+    float v[8] = {};
+    for (int i = 0; i < p.parts; ++i) {
+      float w[8];
+      load8<false>(p.v + ((size_t)i * p.cap + row) * p.rank + q, 0, w);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) v[x] += w[x];
+    }
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      float w[8];
+      load8<true>(b + y * p.rank + q, 0, w);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) o[y] = fmaf(v[x], w[x], o[y]);
+    }
+  }
 }
 
 // sigmoid(g) as a product of two factors, and 1 - sigmoid(g). kFar: from t =
@@ -307,126 +334,101 @@ __device__ void expert_lists(const Args& p, int nslots, ExpertLists& t) {
 // ---- few rows: operands straight from memory --------------------------------
 //
 // The columns' operand is read once, and sets the pace. A workgroup computes
-// 16 outputs of 16 RT rows; its four waves take a quarter of the reduction
-// each, 128 elements at a time by turns, so that 16 rows of 1 KB are in flight,
-// and add up in LDS. v_mfma_f32_16x16x32_bf16: a lane (r = lane % 16, g = lane
+// 16 outputs of 16 rows; its waves take 32 U elements of the reduction at a
+// time by turns, and add up in LDS. v_mfma_f32_16x16x32_bf16: a lane (r = lane % 16, g = lane
 // / 16) holds elements 8g.. of row r of 32, and ends with outputs 4g.. of row r.
 __device__ __forceinline__ f32x4 mfma_few(i32x4 a, i32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
                                                  __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-constexpr int kFewStep = 128;
 
-template <int kMode, bool kBF16, int RT>
-__global__ __launch_bounds__(kExpertThreads) void k_bf16_few(TileArgs p) {
+template <int kMode, bool kBF16, int kWaves, int U>
+__global__ __launch_bounds__(64 * kWaves) void k_bf16_few(TileArgs p) {
   constexpr bool kLora = kMode == kTileLora, kGated = kMode == kTileGated;
   constexpr int NG = kGated ? 2 : 1;  // weight rows to an output
-  constexpr int U = kFewStep / 32;
-  __shared__ f32x4 sums[4][NG * RT][64];
+  constexpr int kStep = 32 * U;
+  static_assert(kLora || 64 * kWaves == kExpertThreads, "the threads that make the tile table");
+  __shared__ f32x4 sums[kWaves][NG][64];
   __shared__ int first[kLora ? 1 : kMaxPlanSlots + 1];
-  __shared__ int part[kExpertThreads / 64];
+  __shared__ int part[kWaves];
   if (!kLora && (p.status[0] & MB_ST_FATAL)) return;
   const int nslots = p.P * p.NS;
-  if constexpr (!kLora) tile_table<16 * RT>(p, nslots, first, part);
+  if constexpr (!kLora) tile_table<16>(p, nslots, first, part);
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int ntn = (p.n + 15) / 16;
-  const int64_t total =
-      (int64_t)(kLora ? (p.cap + 16 * RT - 1) / (16 * RT) : first[nslots]) * ntn;
+  const int64_t total = (int64_t)(kLora ? (p.cap + 15) / 16 : first[nslots]) * ntn;
   for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
     const int mt = (int)(t / ntn), n0 = (int)(t - (int64_t)mt * ntn) * 16;
-    int lo = 0, hi = p.cap, e = 0, m0 = mt * 16 * RT;
+    int lo = 0, hi = p.cap, e = 0, m0 = mt * 16;
     if constexpr (!kLora) {
       const int j = slot_of(first, nslots, mt);
       slot_rows(p, j, lo, hi, e);
-      m0 = lo + (mt - first[j]) * 16 * RT;
+      m0 = lo + (mt - first[j]) * 16;
     }
     // rows past the slot's or the weights' end read the last one instead
-    const uint16_t *w[NG], *a[RT];
+    const uint16_t* w[NG];
 #pragma unroll
     for (int i = 0; i < NG; ++i)
       w[i] = p.w + (((int64_t)e * NG + i) * p.n + min(n0 + r, p.n - 1)) * p.k + g * 8;
-#pragma unroll
-    for (int i = 0; i < RT; ++i) a[i] = p.a + (int64_t)min(m0 + i * 16 + r, hi - 1) * p.k + g * 8;
-    f32x4 acc[NG * RT] = {};
-    int k = wave * kFewStep;
-    for (; k + kFewStep <= p.k; k += 4 * kFewStep) {
-      i32x4 wv[NG][U], av[RT][U];
+    const uint16_t* a = p.a + (int64_t)min(m0 + r, hi - 1) * p.k + g * 8;
+    f32x4 acc[NG] = {};
+    int k = wave * kStep;
+    for (; k + kStep <= p.k; k += kWaves * kStep) {
+      i32x4 wv[NG][U], av[U];
 #pragma unroll
       for (int i = 0; i < NG; ++i)
 #pragma unroll
         for (int u = 0; u < U; ++u) wv[i][u] = load16(w[i] + k + u * 32);
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int u = 0; u < U; ++u) av[i][u] = load16(a[i] + k + u * 32);
+      for (int u = 0; u < U; ++u) av[u] = load16(a + k + u * 32);
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-          for (int o = 0; o < NG; ++o)
-            acc[i * NG + o] = mfma_few(wv[o][u], av[i][u], acc[i * NG + o]);
+        for (int i = 0; i < NG; ++i) acc[i] = mfma_few(wv[i][u], av[u], acc[i]);
     }
     for (; k < p.k; k += 32) {  // the wave whose turn the rest of the rows is
       const bool in = k + g * 8 < p.k;
-      i32x4 wv[NG];
+      const i32x4 av = in ? load16(a + k) : i32x4{};
 #pragma unroll
-      for (int o = 0; o < NG; ++o) wv[o] = in ? load16(w[o] + k) : i32x4{};
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const i32x4 av = in ? load16(a[i] + k) : i32x4{};
-#pragma unroll
-        for (int o = 0; o < NG; ++o) acc[i * NG + o] = mfma_few(wv[o], av, acc[i * NG + o]);
-      }
+      for (int i = 0; i < NG; ++i)
+        acc[i] = mfma_few(in ? load16(w[i] + k) : i32x4{}, av, acc[i]);
     }
 #pragma unroll
-    for (int i = 0; i < NG * RT; ++i) sums[wave][i][lane] = acc[i];
+    for (int i = 0; i < NG; ++i) sums[wave][i][lane] = acc[i];
     __syncthreads();
-    for (int i = wave; i < RT; i += 4) {
+    if (wave == 0) {
       f32x4 o[NG];
 #pragma unroll
-      for (int q = 0; q < NG; ++q)
-        o[q] = (sums[0][i * NG + q][lane] + sums[1][i * NG + q][lane]) +
-               (sums[2][i * NG + q][lane] + sums[3][i * NG + q][lane]);
-      const int m = m0 + i * 16 + r, nn = n0 + 4 * g;
-      float h[4];
+      for (int i = 0; i < NG; ++i) {
+        o[i] = sums[0][i][lane];
+#pragma unroll
+        for (int x = 1; x < kWaves; ++x) o[i] += sums[x][i][lane];
+      }
+      const int m = m0 + r, nn = n0 + 4 * g;
+      float h[4] = {o[0][0], o[0][1], o[0][2], o[0][3]};
       if constexpr (kGated) {
-        const float x[4] = {o[0][0], o[0][1], o[0][2], o[0][3]};
+        const float x[4] = {h[0], h[1], h[2], h[3]};
         const float u[4] = {o[1][0], o[1][1], o[1][2], o[1][3]};
         gated<4>(x, u, h);
       }
       if constexpr (kLora) {
-        const int row = min(m, hi - 1), id = adapter_of(p, row);
-        for (int ad = -1;;) {
-          ad = wave_min_i32(id > ad ? id : INT32_MAX);
-          if (ad == INT32_MAX) break;
-          for (int q = 0; q < p.rank; q += 32) {
-            const int at = q + g * 8;
-            i32x4 b = {}, v[3];
-            if (n0 + r < p.n && at < p.rank)
-              b = load16(p.b + ((size_t)ad * p.n + n0 + r) * p.rank + at);
-            load_v(p, row, at, id == ad, v);
-#pragma unroll
-            for (int x = 0; x < 3; ++x) o[0] = mfma_few(b, v[x], o[0]);
-          }
-        }
+        if (nn < p.n) add_adapter(p, min(m, hi - 1), nn, h);
       }
       if (m < hi && nn < p.n) {
-        if constexpr (kGated) {
+        if constexpr (kBF16)
           *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + (size_t)m * p.n + nn) =
               uint2{bf16x2_rne(h[0], h[1]), bf16x2_rne(h[2], h[3])};
+        else
+          *reinterpret_cast<f32x4*>(static_cast<float*>(p.y) + (size_t)m * p.n + nn) =
+              f32x4{h[0], h[1], h[2], h[3]};
+        if constexpr (kGated) {
           if (p.pre)
 #pragma unroll
-            for (int q = 0; q < NG; ++q)
-              *reinterpret_cast<uint2*>(p.pre + ((size_t)m * NG + q) * p.n + nn) =
-                  uint2{bf16x2_rne(o[q][0], o[q][1]), bf16x2_rne(o[q][2], o[q][3])};
-        } else if constexpr (kBF16) {
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + (size_t)m * p.n + nn) =
-              uint2{bf16x2_rne(o[0][0], o[0][1]), bf16x2_rne(o[0][2], o[0][3])};
-        } else {
-          *reinterpret_cast<f32x4*>(static_cast<float*>(p.y) + (size_t)m * p.n + nn) = o[0];
+            for (int i = 0; i < NG; ++i)
+              *reinterpret_cast<uint2*>(p.pre + ((size_t)m * NG + i) * p.n + nn) =
+                  uint2{bf16x2_rne(o[i][0], o[i][1]), bf16x2_rne(o[i][2], o[i][3])};
         }
       }
     }
@@ -500,7 +502,8 @@ __device__ __forceinline__ void wait_stores() {
 template <int kMode, bool kBF16, int JT>
 __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
   constexpr int BM = 64 * JT;
-  constexpr bool kLora = kMode == kTileLora, kGated = kMode == kTileGated;
+  constexpr bool kSplit = kMode == kTileSplit, kLora = kMode == kTileLora || kSplit;
+  constexpr bool kGated = kMode == kTileGated;
   constexpr bool kGateGrad = kMode == kTileGateGrad, kAdd = kMode == kTileWeightAdd;
   constexpr bool kSum = kMode == kTileWeightGrad || kAdd;
   constexpr bool kColW = kMode == kTileRowGrad || kGateGrad || kSum, kColA = kSum;
@@ -525,7 +528,7 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
     total = mtiles * ntn * p.E;
   } else if constexpr (kLora) {
     mtiles = (p.cap + BM - 1) / BM;
-    total = mtiles * ntn;
+    total = mtiles * ntn * (kSplit ? p.splits : 1);
   } else {
     slot_table<BM>(p, nslots, table, part);
     mtiles = uniform(table.first[nslots]);
@@ -541,7 +544,7 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
   auto tile_of = [&](int t) {
     BfTile o;
     int e = 0;
-    if constexpr (kSum) {
+    if constexpr (kSum || kSplit) {
       e = uniform(t / (mtiles * ntn));
       t -= e * mtiles * ntn;
     }
@@ -565,6 +568,8 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
   auto stages_of = [&](int e) {
     if constexpr (kSum)
       return uniform(table.stages[e]);
+    else if constexpr (kSplit)
+      return min(p.split_stages, (p.k + 63) / 64 - e * p.split_stages);
     else
       return (p.k + 63) / 64;
   };
@@ -646,7 +651,13 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
         ow = {p.w + (((int64_t)t.e * 2 + (wave & 1)) * p.n + n) * p.k, nn * pw, 0};
       } else {
         const int n = t.n0 + wave * 64, nn = uniform(min(max(p.n - n, 0), 64));
-        ow = {p.w + ((int64_t)t.e * p.n + n) * p.k, nn * pw, 0};
+        if constexpr (kSplit) {  // from the part's first element of every row
+          const int k0 = t.e * p.split_stages * 64;
+          oa = {p.a + (int64_t)m * p.k + k0, nm * pa - k0 * 2, 0};
+          ow = {p.w + (int64_t)n * p.k + k0, nn * pw - k0 * 2, 0};
+        } else {
+          ow = {p.w + ((int64_t)t.e * p.n + n) * p.k, nn * pw, 0};
+        }
       }
     }
   };
@@ -684,7 +695,9 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
     uint32_t at[2];
     int step;
   };
-  auto last_stage = [&] { return c_left == 1 ? 0xffffffffu : 0u; };  // of a tile
+  auto last_stage = [&] {  // of a row
+    return c_left == 1 && (!kSplit || at0.e == p.splits - 1) ? 0xffffffffu : 0u;
+  };
   auto offsets_w = [&](Copies& c) {
     const int pitch = fresh(pw);
 #pragma unroll
@@ -871,7 +884,7 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < JN; ++j) asm volatile("" : "+a"(acc[i][j]));
-    if constexpr (kLora) {
+    if constexpr (kLora && !kSplit) {
       // the reduction goes on over the ranks of every adapter among the
       // wave's rows, with zeros in the rows of the others
       int row[JN], id[JN];
@@ -958,7 +971,7 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
     } else {
       const int wide = kGateGrad ? 2 * p.n : p.n;
       const int pitch = fresh(wide * kElt), half = fresh(p.n * 2), end = kGateGrad ? half : pitch;
-      const size_t m = (kSum ? (size_t)tile.e * p.k : 0) + tile.m0;
+      const size_t m = (kSum ? (size_t)tile.e * p.k : kSplit ? (size_t)tile.e * p.cap : 0) + tile.m0;
       uint8_t* const to = static_cast<uint8_t*>(p.y) + m * pitch;
       const RowBuffer y(to, rows, pitch);
       const RowBuffer in(kGateGrad ? static_cast<void*>(p.pre + m * wide) : to,

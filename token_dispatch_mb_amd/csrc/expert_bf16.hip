@@ -26,7 +26,7 @@ void launch_tiles(const TileArgs& p, int64_t rows, hipStream_t st) {
   const dim3 grid(kCus), block(kExpertThreads);
   if constexpr (kMode == kTileProduct || kMode == kTileGated) {
     if (rows < slots * 2) {
-      hipLaunchKernelGGL((k_bf16_few<kMode, kBF16, 1>), dim3(kFewGroups), block, 0, st, p);
+      hipLaunchKernelGGL((k_bf16_few<kMode, kBF16, 4, 4>), dim3(kFewGroups), block, 0, st, p);
       return;
     }
   }

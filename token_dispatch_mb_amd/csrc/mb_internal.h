@@ -154,11 +154,11 @@ hipError_t launch_expert_bf16_wgrad(const mb_dims& d, const Geometry& g, const m
 hipError_t launch_combine_grad(const mb_dims& d, const mb_plan_bufs& o, const void* dy,
                                const void* ye, const float* w, void* dye, float* dw,
                                hipStream_t st);
-// v: lora_parts(p) * rows * rank floats of scratch.
-int lora_parts(const mb_lora_params& p);
+// ws: lora_workspace_floats(p) floats of scratch.
+size_t lora_workspace_floats(const mb_lora_params& p);
 hipError_t launch_project_lora(const mb_lora_params& p, const uint16_t* x, const uint16_t* w,
                                const uint16_t* a, const uint16_t* b, const float* scale,
-                               const int32_t* adapter, float* v, void* y, hipStream_t st);
+                               const int32_t* adapter, float* ws, void* y, hipStream_t st);
 
 // Launch KERNEL<K> for the top-K values with a specialised kernel, KERNEL<0>
 // (runtime K) otherwise.
