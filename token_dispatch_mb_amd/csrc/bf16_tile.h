@@ -885,39 +885,50 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_bf16_tile(TileArgs p) {
 #pragma unroll
       for (int j = 0; j < JN; ++j) asm volatile("" : "+a"(acc[i][j]));
     if constexpr (kLora && !kSplit) {
-      // the reduction goes on over the ranks of every adapter among the
-      // wave's rows, with zeros in the rows of the others
-      int row[JN], id[JN];
+      // the reduction goes on over the ranks of the rows' adapters, 32 rows at
+      // a time. In runs they are all of one; else each adapter's part is made
+      // for all and taken by its rows alone, so that what is not finite in
+      // one stays out of the others.
 #pragma unroll
       for (int j = 0; j < JN; ++j) {
-        row[j] = min(tile.m0 + (2 * j + hm) * 32 + r, tile.hi - 1);
-        id[j] = adapter_of(p, row[j]);
-      }
-      for (int ad = -1;;) {
-        int least = INT32_MAX;
+        const int row = min(tile.m0 + (2 * j + hm) * 32 + r, tile.hi - 1), id = adapter_of(p, row);
+        auto ranks = [&](int ad, f32x16& c0, f32x16& c1, f32x16& c2, f32x16& c3) {
+          for (int q = 0; q < p.rank; q += 16) {
+            const int at = q + h * 8;
+            i32x4 b[4], v[3];
 #pragma unroll
-        for (int j = 0; j < JN; ++j)
-          if (id[j] > ad) least = min(least, id[j]);
-        ad = wave_min_i32(least);
-        if (ad == INT32_MAX) break;
-        for (int q = 0; q < p.rank; q += 16) {
-          const int at = q + h * 8;
-          i32x4 b[4];
+            for (int i = 0; i < 4; ++i) {
+              const int n = tile.n0 + hn * 128 + i * 32 + swapped;
+              b[i] = i32x4{};
+              if (n < p.n && at < p.rank)
+                b[i] = load16(p.b + ((size_t)ad * p.n + n) * p.rank + at);
+            }
+            load_v(p, row, at, id == ad, v);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int n = tile.n0 + hn * 128 + i * 32 + swapped;
-            b[i] = i32x4{};
-            if (n < p.n && at < p.rank) b[i] = load16(p.b + ((size_t)ad * p.n + n) * p.rank + at);
+            for (int x = 0; x < 3; ++x) {
+              c0 = mfma_bf16(b[0], v[x], c0);
+              c1 = mfma_bf16(b[1], v[x], c1);
+              c2 = mfma_bf16(b[2], v[x], c2);
+              c3 = mfma_bf16(b[3], v[x], c3);
+            }
+          }
+        };
+        int ad = wave_min_i32(id);
+        if (__ballot(id == ad) == ~0ull) {
+          if (ad != INT32_MAX) ranks(ad, acc[0][j], acc[1][j], acc[2][j], acc[3][j]);
+        } else {
+          f32x16 sum[4] = {};
+          while (ad != INT32_MAX) {
+            f32x16 one[4] = {};
+            ranks(ad, one[0], one[1], one[2], one[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int x = 0; x < 16; ++x) sum[i][x] = id == ad ? one[i][x] : sum[i][x];
+            ad = wave_min_i32(id > ad ? id : INT32_MAX);
           }
 #pragma unroll
-          for (int j = 0; j < JN; ++j) {
-            i32x4 v[3];
-            load_v(p, row[j], at, id[j] == ad, v);
-#pragma unroll
-            for (int x = 0; x < 3; ++x)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[i][j] = mfma_bf16(b[i], v[x], acc[i][j]);
-          }
+          for (int i = 0; i < 4; ++i) acc[i][j] += sum[i];
         }
       }
     }

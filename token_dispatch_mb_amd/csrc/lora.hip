@@ -157,7 +157,7 @@ Shape shape_of(const mb_lora_params& p) {
   s.few = p.n_rows <= 16;
   const int64_t columns = (p.n_out + kTileN - 1) / kTileN;
   s.tile_rows = p.n_rows > 128 && (p.n_rows + 255) / 256 * columns >= kCus / 16 ? 256 : 128;
-  const int64_t tiles = (p.n_rows + s.tile_rows - 1) / s.tile_rows * columns;
+  const int64_t tiles = std::max<int64_t>(1, (p.n_rows + s.tile_rows - 1) / s.tile_rows * columns);
   const int stages = (p.k_in + 63) / 64;
   // parts of at least four stages, as many as the CUs take at once
   const int most = std::max<int>(1, std::min<int64_t>(stages / 4, kCus / tiles));
