@@ -68,22 +68,33 @@ __global__ __launch_bounds__(kExpertThreads) void k_lora_down(DownArgs p) {
         a[i] = p.a + ((int64_t)ad * p.rank + min(q + i * 16 + r, p.rank - 1)) * p.k + g * 8;
       f32x4 acc[RT][MT] = {};
       int k = k0 + wave * kDownStep;
-      for (; k + kDownStep <= k1; k += 4 * kDownStep) {
-        i32x4 xv[MT][U], av[RT][U];
+      // the next turn's operands are under way while this one's are multiplied
+      i32x4 xv[2][MT][U], av[2][RT][U];
+      auto fetch = [&](int to, int at) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int u = 0; u < U; ++u) xv[i][u] = load16(x[i] + k + u * 32);
+          for (int u = 0; u < U; ++u) xv[to][m][u] = load16(x[m] + at + u * 32);
 #pragma unroll
         for (int i = 0; i < RT; ++i)
 #pragma unroll
-          for (int u = 0; u < U; ++u) av[i][u] = load16(a[i] + k + u * 32);
+          for (int u = 0; u < U; ++u) av[to][i][u] = load16(a[i] + at + u * 32);
+      };
+      if (k + kDownStep <= k1) fetch(0, k);
+      while (k + kDownStep <= k1) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int y = 0; y < 2; ++y) {
+          if (k + kDownStep > k1) break;
+          if (k + 5 * kDownStep <= k1) fetch(y ^ 1, k + 4 * kDownStep);
 #pragma unroll
-          for (int i = 0; i < RT; ++i)
+          for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int m = 0; m < MT; ++m) acc[i][m] = mfma_few(av[i][u], xv[m][u], acc[i][m]);
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+              for (int m = 0; m < MT; ++m)
+                acc[i][m] = mfma_few(av[y][i][u], xv[y][m][u], acc[i][m]);
+          k += 4 * kDownStep;
+        }
       }
       for (; k < k1; k += 32) {
         const bool in = k + g * 8 < k1;
