@@ -436,6 +436,10 @@ __global__ __launch_bounds__(64 * kWaves) void k_bf16_few(TileArgs p) {
   }
 }
 
+// What a stage of 256 rows costs, in eighths of one of 128 (measured: 1.6 to
+// 1.9 times as much, the less the fewer CUs work).
+constexpr int kLongTile = 13;
+
 // ---- tiles staged through LDS ------------------------------------------------
 struct BfTile {
   int m0, hi, n0, e;

@@ -18,19 +18,35 @@ TileArgs plan_args(const mb_dims& d, const Geometry& g, const mb_plan_bufs& o) {
   return p;
 }
 
-// 128 or 256 rows to a tile, from the rows expected in a slot.
+// Whether 256 rows to a tile take less time than 128: in rounds over the CUs,
+// of which one of 256 rows takes kLongTile / 8 times as long.
+bool long_tiles(int64_t tiles256, int64_t tiles128) {
+  return (tiles256 + kCus - 1) / kCus * kLongTile <= (tiles128 + kCus - 1) / kCus * 8;
+}
+
+// From the rows expected in a slot, and 32 more, half of the 64 that tiles leave
+// out of a slot's last one at a time.
+//
+// Few rows: 64 slots, the products of 4096 x 2048 and back: 256 rows 531 us,
+// in tiles 630; 512 rows 645 and 675; 1024 rows 965 and 765.
+// 128 and 256 rows to a tile, the same: 4096 rows 706 and 715 us, 8192 rows
+// 795 and 768, 32768 rows 1830 and 1617; one slot, 7168 x 4096 and back: 1024
+// rows 180 and 277, 2048 rows 326 and 290, 4096 rows 627 and 562.
 template <int kMode, bool kBF16>
 void launch_tiles(const TileArgs& p, int64_t rows, hipStream_t st) {
   const int64_t slots = (int64_t)p.P * p.NS;
-  const int64_t columns = (p.n + kTileN - 1) / kTileN;
+  const int64_t across = kMode == kTileGated ? kTileN / 2 : kTileN;
+  const int64_t columns = (p.n + across - 1) / across;
   const dim3 grid(kCus), block(kExpertThreads);
   if constexpr (kMode == kTileProduct || kMode == kTileGated) {
-    if (rows < slots * 2) {
+    if (rows <= slots * 8) {
       hipLaunchKernelGGL((k_bf16_few<kMode, kBF16, 4, 4>), dim3(kFewGroups), block, 0, st, p);
       return;
     }
   }
-  if (rows >= slots * 160 && (rows / 256 + slots) * columns > 2 * kCus)
+  const int64_t all = rows + slots / 2 * 64;
+  auto tiles = [&](int64_t tall) { return (all + tall - 1) / tall * columns; };
+  if (rows >= slots * 128 && long_tiles(tiles(256), tiles(128)))
     hipLaunchKernelGGL((k_bf16_tile<kMode, kBF16, 4>), grid, block, 0, st, p);
   else
     hipLaunchKernelGGL((k_bf16_tile<kMode, kBF16, 2>), grid, block, 0, st, p);
@@ -77,8 +93,11 @@ hipError_t launch_expert_bf16_wgrad(const mb_dims& d, const Geometry& g, const m
                                     hipStream_t st) {
   TileArgs p = plan_args(d, g, o);
   p.a = dy, p.w = a, p.y = dw, p.n = k_in, p.k = n_out;
-  // 256 rows to a tile where they occupy the CUs
-  const int64_t tiles = (int64_t)p.E * ((p.k + 255) / 256) * ((p.n + kTileN - 1) / kTileN);
+  // (one expert, 2048 rows, both gradients: 4096 x 4096 151 us with 128 rows to
+  // a tile, 137 with 256; 4096 x 2048, half the tiles, 106 and 171)
+  auto tiles = [&](int64_t tall) {
+    return (int64_t)p.E * ((p.k + tall - 1) / tall) * ((p.n + kTileN - 1) / kTileN);
+  };
 #define MB_W(BF16, JT)                                                                       \
   do {                                                                                       \
     if (add)                                                                                 \
@@ -87,7 +106,7 @@ hipError_t launch_expert_bf16_wgrad(const mb_dims& d, const Geometry& g, const m
       hipLaunchKernelGGL((k_bf16_tile<kTileWeightGrad, BF16, JT>), grid, block, 0, st, p);   \
   } while (0)
   const dim3 grid(kCus), block(kExpertThreads);
-  if (tiles >= kCus) {
+  if (long_tiles(tiles(256), tiles(128))) {
     if (bf16) MB_W(true, 4);
     else MB_W(false, 4);
   } else {

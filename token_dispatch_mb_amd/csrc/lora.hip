@@ -24,28 +24,28 @@ struct DownArgs {
   int rows, k, rank, L, parts;
 };
 
-// v of 16 MT rows and 16 RT ranks, of one of their adapters or of one after
-// the other: workgroup (x, y, z) takes the row block x, adapters y, y +
-// gridDim.y, ... in the order of their numbers, and part z of the reduction.
-// Its four waves take 128 elements by turns and add up in LDS. Rows without an
-// adapter are not written (nothing reads them). MT = 4 passes a third as much
-// of the adapters through the caches as MT = 1.
-template <int RT, int MT>
+// v of 16 rows and 16 RT ranks, of one of their adapters or of one after the
+// other: workgroup (x, y, z) takes the row block x, adapters y, y + gridDim.y,
+// ... in the order of their numbers, and part z of the reduction. Its four
+// waves take 128 elements by turns, the next turn's on their way while this
+// one's are multiplied, and add up in LDS. Rows without an adapter are not
+// written (nothing reads them).
+//
+// Bound by the reading of x and of the adapters, which every row block passes
+// again, from the caches: 16384 rows of 7168 elements in 54, 95 and 178 us at
+// rank 16, 32 and 64 (4.3, 2.5 TB/s of x). 64 rows to a workgroup pass the
+// adapters a quarter as often and took 65, 79 and 152 us, and at 4096 rows,
+// where too few workgroups are left, 64, 77 and 224 us for 28, 40 and 77.
+template <int RT>
 __global__ __launch_bounds__(kExpertThreads) void k_lora_down(DownArgs p) {
   constexpr int U = kDownStep / 32;
-  __shared__ f32x4 sums[4][RT * MT][64];
+  __shared__ f32x4 sums[4][RT][64];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  int row[MT], id[MT];
-  const uint16_t* x[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    row[i] = (blockIdx.x * MT + i) * 16 + r;
-    const int at = min(row[i], p.rows - 1);
-    id[i] = p.adapter[at];
-    if ((unsigned)id[i] >= (unsigned)p.L || row[i] >= p.rows) id[i] = INT32_MAX;
-    x[i] = p.x + (int64_t)at * p.k + g * 8;
-  }
+  const int row = blockIdx.x * 16 + r, at = min(row, p.rows - 1);
+  int id = p.adapter[at];
+  if ((unsigned)id >= (unsigned)p.L || row >= p.rows) id = INT32_MAX;
+  const uint16_t* x = p.x + (int64_t)at * p.k + g * 8;
   // part z: whole turns of four waves
   const int turns = (p.k + 4 * kDownStep - 1) / (4 * kDownStep);
   const int each = (turns + p.parts - 1) / p.parts;
@@ -53,11 +53,7 @@ __global__ __launch_bounds__(kExpertThreads) void k_lora_down(DownArgs p) {
   const int k1 = min(k0 + each * 4 * kDownStep, p.k);
   int ad = -1;
   for (int j = 0;; ++j) {
-    int least = INT32_MAX;
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-      if (id[i] > ad) least = min(least, id[i]);
-    ad = wave_min_i32(least);
+    ad = wave_min_i32(id > ad ? id : INT32_MAX);
     if (ad == INT32_MAX) break;
     if (j % gridDim.y != blockIdx.y) continue;
     const float scale = p.scale[ad];
@@ -66,15 +62,12 @@ __global__ __launch_bounds__(kExpertThreads) void k_lora_down(DownArgs p) {
 #pragma unroll
       for (int i = 0; i < RT; ++i)
         a[i] = p.a + ((int64_t)ad * p.rank + min(q + i * 16 + r, p.rank - 1)) * p.k + g * 8;
-      f32x4 acc[RT][MT] = {};
+      f32x4 acc[RT] = {};
       int k = k0 + wave * kDownStep;
-      // the next turn's operands are under way while this one's are multiplied
-      i32x4 xv[2][MT][U], av[2][RT][U];
+      i32x4 xv[2][U], av[2][RT][U];
       auto fetch = [&](int to, int at) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int u = 0; u < U; ++u) xv[to][m][u] = load16(x[m] + at + u * 32);
+        for (int u = 0; u < U; ++u) xv[to][u] = load16(x + at + u * 32);
 #pragma unroll
         for (int i = 0; i < RT; ++i)
 #pragma unroll
@@ -89,40 +82,27 @@ __global__ __launch_bounds__(kExpertThreads) void k_lora_down(DownArgs p) {
 #pragma unroll
           for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < RT; ++i)
-#pragma unroll
-              for (int m = 0; m < MT; ++m)
-                acc[i][m] = mfma_few(av[y][i][u], xv[y][m][u], acc[i][m]);
+            for (int i = 0; i < RT; ++i) acc[i] = mfma_few(av[y][i][u], xv[y][u], acc[i]);
           k += 4 * kDownStep;
         }
       }
       for (; k < k1; k += 32) {
         const bool in = k + g * 8 < k1;
-        i32x4 xv[MT];
+        const i32x4 xs = in ? load16(x + k) : i32x4{};
 #pragma unroll
-        for (int m = 0; m < MT; ++m) xv[m] = in ? load16(x[m] + k) : i32x4{};
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          const i32x4 av = in ? load16(a[i] + k) : i32x4{};
-#pragma unroll
-          for (int m = 0; m < MT; ++m) acc[i][m] = mfma_few(av, xv[m], acc[i][m]);
-        }
+        for (int i = 0; i < RT; ++i)
+          acc[i] = mfma_few(in ? load16(a[i] + k) : i32x4{}, xs, acc[i]);
       }
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) sums[wave][i * MT + m][lane] = acc[i][m];
+      for (int i = 0; i < RT; ++i) sums[wave][i][lane] = acc[i];
       __syncthreads();
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-        for (int i = 0; i < RT; ++i) {
-          if (((i * MT + m) & 3) != wave) continue;
-          const f32x4 s = ((sums[0][i * MT + m][lane] + sums[1][i * MT + m][lane]) +
-                           (sums[2][i * MT + m][lane] + sums[3][i * MT + m][lane])) * scale;
-          const int o = q + i * 16 + 4 * g;
-          if (id[m] == ad && o < p.rank)
-            *reinterpret_cast<f32x4*>(p.v + ((size_t)blockIdx.z * p.rows + row[m]) * p.rank + o) = s;
-        }
+      if (wave < RT) {
+        const f32x4 s = ((sums[0][wave][lane] + sums[1][wave][lane]) +
+                         (sums[2][wave][lane] + sums[3][wave][lane])) * scale;
+        const int o = q + wave * 16 + 4 * g;
+        if (id == ad && o < p.rank)
+          *reinterpret_cast<f32x4*>(p.v + ((size_t)blockIdx.z * p.rows + row) * p.rank + o) = s;
+      }
       __syncthreads();
     }
   }
@@ -159,20 +139,49 @@ struct Shape {
   size_t v, parts;           // floats
 };
 
+int64_t tiles_of(const mb_lora_params& p, int rows) {
+  return ((int64_t)p.n_rows + rows - 1) / rows * ((p.n_out + kTileN - 1) / kTileN);
+}
+
+// In eighths of a microsecond, roughly: a stage of a 128-row tile takes eight,
+// of a 256-row tile kLongTile; where there are parts, a launch takes 3 us and
+// their sums are written and read back at 5 TB/s.
+int64_t tiles_cost(const mb_lora_params& p, int rows, int splits) {
+  const int64_t tiles = tiles_of(p, rows);
+  const int stages = ((p.k_in + 63) / 64 + splits - 1) / splits;
+  const int64_t cost = (tiles * splits + kCus - 1) / kCus * stages * (rows == 256 ? kLongTile : 8);
+  return cost + (splits > 1 ? 24 + (int64_t)splits * p.n_rows * p.n_out / 80000 : 0);
+}
+
 Shape shape_of(const mb_lora_params& p) {
   Shape s = {};
-  // few rows would leave most CUs idle: more parts
+  // few rows would leave most CUs idle: more parts (64 rows of 7168 elements,
+  // rank 16: 15.5 us in one part, 9.6 in four; 4096 rows: 28 and 20, but the
+  // product reads v four times)
   const int blocks = (p.n_rows + 15) / 16, turns = (p.k_in + 4 * kDownStep - 1) / (4 * kDownStep);
   s.down_parts = blocks >= 64 ? 1 : std::min(turns, 4);
   s.v = (size_t)s.down_parts * p.n_rows * p.rank;
-  s.few = p.n_rows <= 16;
-  const int64_t columns = (p.n_out + kTileN - 1) / kTileN;
-  s.tile_rows = p.n_rows > 128 && (p.n_rows + 255) / 256 * columns >= kCus / 16 ? 256 : 128;
-  const int64_t tiles = std::max<int64_t>(1, (p.n_rows + s.tile_rows - 1) / s.tile_rows * columns);
+  // 16 rows, n_out = k_in = 4096: 19 us (tiles: 25); 24 rows: 28 (27). Small
+  // products leave CUs idle in tiles (32 rows, 1024: 16 us, tiles 20).
+  s.few = p.n_rows <= 16 || (int64_t)blocks * ((p.n_out + 15) / 16) < kCus;
+  // else the cheapest of both tiles and of up to as many parts as the CUs take
+  // at once, of at least four stages. n_out = k_in = 7168, the best of 128-row
+  // tiles against 256-row tiles, us: 384 rows 74, 85; 1024 rows 123, 151;
+  // 4096 rows 486, 473; of one part against several: 512 rows 121, 87; 2048 x
+  // 2048 x 2048: 51, 58.
   const int stages = (p.k_in + 63) / 64;
-  // parts of at least four stages, as many as the CUs take at once
-  const int most = std::max<int>(1, std::min<int64_t>(stages / 4, kCus / tiles));
-  s.split_stages = (stages + most - 1) / most;
+  int64_t best = INT64_MAX;
+  for (int rows = 128; rows <= 256; rows += 128) {
+    const int64_t tiles = std::max<int64_t>(1, tiles_of(p, rows));
+    const int most = std::max<int>(1, std::min<int64_t>(stages / 4, kCus / tiles));
+    for (int splits = 1; splits <= most; ++splits) {
+      const int64_t cost = tiles_cost(p, rows, splits);
+      if (cost >= best) continue;
+      best = cost;
+      s.tile_rows = rows;
+      s.split_stages = (stages + splits - 1) / splits;
+    }
+  }
   s.splits = (stages + s.split_stages - 1) / s.split_stages;
   s.parts = s.few || s.splits == 1 ? 0 : (size_t)s.splits * p.n_rows * p.n_out;
   return s;
@@ -198,19 +207,12 @@ hipError_t launch_project_lora(const mb_lora_params& q, const uint16_t* x, const
   float* const parts = ws + (s.v + 63) / 64 * 64;
   const DownArgs d = {x, a, scale, adapter, ws, q.n_rows, q.k_in, q.rank, q.n_adapters, p.parts};
   const int blocks = (q.n_rows + 15) / 16;
-  if (s.down_parts > 1 || blocks < kCus) {
-    const dim3 grid(blocks, blocks >= 64 ? 4 : 16, s.down_parts);
-    if (q.rank <= 16)
-      hipLaunchKernelGGL((k_lora_down<1, 1>), grid, block, 0, st, d);
-    else
-      hipLaunchKernelGGL((k_lora_down<2, 1>), grid, block, 0, st, d);
-  } else {
-    const dim3 grid((blocks + 3) / 4);
-    if (q.rank <= 16)
-      hipLaunchKernelGGL((k_lora_down<1, 4>), grid, block, 0, st, d);
-    else
-      hipLaunchKernelGGL((k_lora_down<2, 4>), grid, block, 0, st, d);
-  }
+  // (a block's rows have up to 16 adapters; in long batches, mostly one)
+  const dim3 down(blocks, blocks >= 64 ? 4 : 16, s.down_parts);
+  if (q.rank <= 16)
+    hipLaunchKernelGGL((k_lora_down<1>), down, block, 0, st, d);
+  else
+    hipLaunchKernelGGL((k_lora_down<2>), down, block, 0, st, d);
   hipError_t rc = hipGetLastError();
   if (rc != hipSuccess) return rc;
   const bool bf16 = q.dtype_out == MB_BF16;
