@@ -597,3 +597,56 @@ def test_binding_checks():
     big = out(max(L.rows * n, L.E * n * n))
     with pytest.raises(ValueError, match="overlap"):
         mb.expert_bf16_wgrad(L.dims, L.bufs, n, n, big[: L.rows * n], y, big)
+
+
+# ------------------------------------------------------------ both sides of what picks a kernel
+
+@pytest.mark.parametrize("counts", [[[3830]], [[1400, 250, 1200, 700]], [[600, 385, 513, 64] * 2]])
+def test_one_round_of_tall_tiles(counts):
+    """Tiles of 256 rows that fill the CUs once, of 128 rows twice."""
+    home = len(counts[0])
+    n, k = 4104, 72
+    for dtype in ("f32", "bf16"):
+        L = Layer(counts, home, pad=1, dtype_out=dtype)
+        run_product(L, n, k, "none", dtype)
+        run_dgrad(L, k, n, "none", dtype)
+    run_dgrad(L, k, n, "swiglu", "bf16")
+    run_product(L, 2056, k, "swiglu", "bf16")
+
+
+@pytest.mark.parametrize("rows", [7, 8, 9, 40])
+def test_rows_in_a_slot_around_the_kernel_for_few(rows):
+    """The same slots, some with far more rows than expected."""
+    for counts in ([[rows] * 3, [rows, 0, 2 * rows]], [[6 * rows, 0, 0], [0, 0, 0]]):
+        L = Layer(counts, 3, pad=2)
+        run_product(L, 264, 520, "swiglu", "bf16")
+        run_product(L, 72, 1032, "none", "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("t,n,k,rank,L", [
+    (3830, 4104, 72, 16, 9),  # tall tiles, the reduction in one
+    (130, 16648, 2000, 16, 9),  # tall tiles, in three parts
+    (100, 1032, 4104, 40, 30), (256, 520, 2056, 256, 4),  # low tiles in parts
+    (300, 520, 136, 16, 5),  # low tiles, the reduction in one
+    (48, 1032, 520, 24, 6), (48, 1352, 520, 24, 6),  # few rows, and past them
+])
+def test_lora_shapes(t, n, k, rank, L, dtype):
+    r = rng(t, n)
+    run_lora(t, n, k, rank, L, r.integers(-1, L, t), dtype)
+    run_lora(t, n, k, rank, L, np.arange(t) // 60 % (L + 1) - 1, dtype, seed=1)
+
+
+@pytest.mark.parametrize("t,n,k", [(64, 1032, 1032), (3830, 4104, 72)])
+def test_lora_infinities_in_one_adapter(t, n, k):
+    r = rng(t)
+    x, w, a, b = bf(r, t, k), bf(r, n, k), bf(r, 2, 8, k), bf(r, 2, n, 8)
+    a[1, 3, 5], b[1, 3, 2] = np.inf, np.nan
+    ad = np.arange(t, dtype=np.int32) % 3 - 1  # none, 0, 1 by turns
+    prm = mb.LoraParams.make(t, n, k, 8, 2, dtype_out="f32")
+    y = out(t, n, dtype="f32")
+    mb.project_lora(prm, dev(x), dev(w), dev(a), dev(b), dev(np.ones(2), torch.float32),
+                    torch.from_numpy(ad).to(G.dev()), mb.alloc_lora_workspace(prm, G.dev()), y)
+    good = np.isfinite(f64(y))
+    assert good[ad != 1].all()
+    assert not good[ad == 1].any()
