@@ -119,8 +119,9 @@ __device__ __forceinline__ void copy16(i32x4 buf, lds_ptr to, uint32_t voff, uin
                : "memory");
 }
 
-// For copies without that wait (copy16<0>): a buffer that has waited. Their
-// kernels must not spill scalar registers.
+// For copies without that wait (copy16<0>): a buffer that has waited. Nothing
+// of theirs may be read back from a vector register close before them, which
+// the disassembled library is tested for.
 __device__ __forceinline__ i32x4 settled(i32x4 buf) {
   asm volatile("s_nop 4" : "+s"(buf));
   return buf;
