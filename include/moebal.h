@@ -635,7 +635,9 @@ size_t mb_lora_workspace_bytes(const mb_lora_params* prm);
  * rounded once (to nearest even). Rows of one adapter need not be consecutive,
  * though a run of them costs less (4096 rows of 64 adapters in turn, 4096 x
  * 4096: 1.9 ms, in runs 0.18). What is not finite in an adapter stays in the
- * rows that have it.
+ * rows that have it, and gives what the formula does: an infinite element of
+ * lora_b is one times any inner sum but 0 (of sums below 2^-94 some may count
+ * as 0).
  *  x_dev        [n_rows, k_in] bf16.
  *  w_dev        [n_out, k_in] bf16.
  *  lora_a_dev   [L, rank, k_in] bf16; lora_b_dev [L, n_out, rank] bf16.

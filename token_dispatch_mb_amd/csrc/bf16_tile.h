@@ -99,7 +99,10 @@ __device__ __forceinline__ int adapter_of(const TileArgs& p, int row) {
 }
 
 // Elements [at, at + 8) of a row of v, each as three bf16 that together hold
-// all of its 24 bits: v is not rounded.
+// all of its 24 bits: v is not rounded. A part is the largest bf16 below what
+// is left, not that itself, so that none of a value's parts is zero: times an
+// infinity they are its sign's. (Of values below 2^-94 a part may be; an
+// infinity or a NaN is all three parts.)
 __device__ __forceinline__ void load_v(const TileArgs& p, int row, int at, bool on, i32x4* v3) {
   float s[8] = {};
   if (on && at < p.rank)
@@ -109,17 +112,21 @@ __device__ __forceinline__ void load_v(const TileArgs& p, int row, int at, bool 
 #pragma unroll
       for (int x = 0; x < 8; ++x) s[x] += v[x];
     }
+  uint32_t part[3][8];
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    const bool finite = fabsf(s[x]) < INFINITY;
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      const uint32_t below = q < 2 && finite && s[x] != 0.0f ? 1 : 0;
+      part[q][x] = (__float_as_uint(s[x]) - below) & 0xffff0000u;
+      if (finite) s[x] -= __uint_as_float(part[q][x]);
+    }
+  }
 #pragma unroll
   for (int q = 0; q < 3; ++q)
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const uint32_t a = __float_as_uint(s[2 * x]) & 0xffff0000u;
-      const uint32_t b = __float_as_uint(s[2 * x + 1]) & 0xffff0000u;
-      v3[q][x] = (int)(a >> 16 | b);
-      // nothing is left of an infinity or a NaN
-      s[2 * x] = fabsf(s[2 * x]) < INFINITY ? s[2 * x] - __uint_as_float(a) : 0.0f;
-      s[2 * x + 1] = fabsf(s[2 * x + 1]) < INFINITY ? s[2 * x + 1] - __uint_as_float(b) : 0.0f;
-    }
+    for (int x = 0; x < 4; ++x) v3[q][x] = (int)(part[q][2 * x] >> 16 | part[q][2 * x + 1]);
 }
 
 // o[0..4) += outputs [n, n + 4) of a row's adapter. A lane by itself: rows may
