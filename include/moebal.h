@@ -579,7 +579,8 @@ int mb_expert_bf16_dgrad(const mb_dims* dims, const mb_plan_bufs* plan, int32_t 
  *  accumulate  non-zero: the sum is added to what dw_dev holds.
  *  dy_dev      [P*cap, n_out] bf16; a_dev [P*cap, k_in] bf16.
  *  dw_dev      [E, n_out, k_in] of dtype.
- * Everything else as mb_expert_bf16 (with N = 0 the plan is read all the same).
+ * Everything else as mb_expert_bf16; with N = 0 no expert has rows, whatever the
+ * plan holds (dy_dev and a_dev may be NULL), and a fatal status still leaves dw_dev.
  */
 int mb_expert_bf16_wgrad(const mb_dims* dims, const mb_plan_bufs* plan, int32_t n_out, int32_t k_in,
                          int32_t dtype, int32_t accumulate, const uint16_t* dy_dev,

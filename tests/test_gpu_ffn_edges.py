@@ -85,3 +85,16 @@ def test_lora_infinities_keep_their_sign(t, n, k, order):
                                got[bad][:4], want[bad][:4])
     good = np.isfinite(want) & (ad != 2)[:, None]
     near(got[good], want[good], F.rounded(want, err, "f32")[good])
+
+
+# ------------------------------------------------------------ weights' gradients
+
+@pytest.mark.parametrize("add", [False, True])
+def test_wgrad_without_tokens_takes_no_rows_of_another_plan(add):
+    L = Layer([[37, 0, 5, 1], [0, 70, 13, 2]], 3)
+    d = mb.Dims.make(0, 1, L.E, L.P, L.R, 128, cap=L.cap)
+    n, k = 72, 40
+    ones = torch.ones(L.rows, n, dtype=torch.bfloat16, device=G.dev())
+    dw = out(L.E, n, k, dtype="f32")
+    mb.expert_bf16_wgrad(d, L.bufs, n, k, ones, ones, dw, accumulate=add)
+    assert marked(dw).all() if add else not f64(dw).any()

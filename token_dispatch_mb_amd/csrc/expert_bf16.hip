@@ -101,6 +101,7 @@ hipError_t launch_expert_bf16_wgrad(const mb_dims& d, const Geometry& g, const m
                                     hipStream_t st) {
   TileArgs p = plan_args(d, g, o);
   p.a = dy, p.w = a, p.y = dw, p.n = k_in, p.k = n_out;
+  if (d.n_tokens == 0) p.cap = 0;  // no rows, though the plan be of another call
   // (one expert, 2048 rows, both gradients: 4096 x 4096 151 us with 128 rows to
   // a tile, 137 with 256; 4096 x 2048, half the tiles, 106 and 171)
   auto tiles = [&](int64_t tall) {
