@@ -98,3 +98,30 @@ def test_wgrad_without_tokens_takes_no_rows_of_another_plan(add):
     dw = out(L.E, n, k, dtype="f32")
     mb.expert_bf16_wgrad(d, L.bufs, n, k, ones, ones, dw, accumulate=add)
     assert marked(dw).all() if add else not f64(dw).any()
+
+
+# ------------------------------------------------------------ far gates
+
+@pytest.mark.parametrize("rows", [3, 64, 300])
+def test_far_gates_of_large_ups_keep_their_value(rows):
+    """silu(g) u where silu(g) alone is below binary32 and u brings it back."""
+    gates = np.array([-170, -150, -130, -110, -104, -95, -88.5, -81, -60, -3, 0.5, 90])
+    ups = 2.0 ** np.array([0, 30, 60, 90, 120])
+    n, k = len(gates) * len(ups) + 4, 8
+    pair = np.array([(g, u) for g in gates for u in ups] + [(1, 1)] * 4)
+    pair = R.bf16_round(np.float32(pair)).astype(np.float64)
+    L = Layer([[rows]], 1)
+    a = np.zeros((rows, k))
+    a[:, 0] = 1
+    w = np.zeros((1, 2 * n, k))
+    w[0, :n, 0], w[0, n:, 0] = pair.T
+    y = out(rows, n)
+    mb.expert_bf16(L.dims, L.bufs, n, k, dev(a), dev(w), y, act="swiglu")
+    g, u = pair.T
+    h = g * F.sigmoid(g) * u
+    # the products of the sums are exact here; the exponential's argument and
+    # result, the reciprocal, four products
+    want = np.broadcast_to(h, (rows, n))
+    fits = np.abs(h) < 2.0**127
+    near(f64(y)[:, fits], want[:, fits],
+         F.rounded(want, np.abs(want) * (F.sigmoid_error(g) + 2.0**-21), "bf16")[:, fits])

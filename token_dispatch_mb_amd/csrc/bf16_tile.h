@@ -184,11 +184,15 @@ __device__ __forceinline__ bool far_gate(const float* g) {
   return __ballot(least < -80.0f) != 0;
 }
 
-// o = silu(g) u
+// o = silu(g) u; far, one of the factors goes to u, so that what the two make
+// together does not vanish where u is large enough to bring it back.
 template <int N, bool kFar>
 __device__ __forceinline__ void gate_of(const float* g, const float* u, float* o) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) o[i] = Sigmoid<kFar>(g[i]).times(g[i]) * u[i];
+  for (int i = 0; i < N; ++i) {
+    const Sigmoid<kFar> s(g[i]);
+    o[i] = kFar ? (g[i] * s.a) * (s.b * u[i]) : s.times(g[i]) * u[i];
+  }
 }
 
 template <int N>
