@@ -125,3 +125,190 @@ def test_far_gates_of_large_ups_keep_their_value(rows):
     fits = np.abs(h) < 2.0**127
     near(f64(y)[:, fits], want[:, fits],
          F.rounded(want, np.abs(want) * (F.sigmoid_error(g) + 2.0**-21), "bf16")[:, fits])
+
+
+# ------------------------------------------------------------ past 2^31 elements
+
+def blank(*shape, dtype=torch.bfloat16):
+    return torch.full(shape, MARK, dtype=dtype, device=G.dev())
+
+
+def untouched(t, rows):
+    """Whether all rows but these still hold the mark (in pieces: the tensors are large)."""
+    keep = torch.ones(t.shape[0], dtype=torch.bool, device=t.device)
+    keep[torch.from_numpy(rows).to(t.device)] = False
+    mark = torch.tensor(MARK, dtype=t.dtype, device=t.device)
+    return all(bool((p == mark).all(1)[k].all()) for p, k in zip(t.split(1 << 17), keep.split(1 << 17)))
+
+
+def region(counts, cap, expected, home=1, dtype_out="bf16"):
+    """A layer whose ranks' regions have `cap` rows, few of them used."""
+    L = Layer(counts, home, pad=cap - int(np.asarray(counts).sum(axis=1).max()), expected=expected,
+              dtype_out=dtype_out)
+    assert L.cap == cap
+    return L, np.flatnonzero(L.used)
+
+
+@pytest.mark.parametrize("expected", [12, 3 << 17])  # operands straight from memory, tiles
+def test_rows_past_two_billion_elements(expected):
+    cap, n, k = 1 << 19, 2056, 72
+    L, used = region([[5], [0], [37]], cap, expected)
+    assert L.rows * n > 1 << 31
+    r = rng(expected)
+    at = torch.from_numpy(used).to(G.dev())
+    thin, wide = bf(r, len(used), k), bf(r, len(used), n)
+    a, y = blank(L.rows, k), blank(L.rows, n)
+    a[at] = dev(thin)
+    w = bf(r, L.E, n, k, std=k**-0.5)
+    rows = {e: np.searchsorted(used, np.arange(lo, hi)) for e, lo, hi in L.groups}
+    mb.expert_bf16(L.dims, L.bufs, n, k, a, dev(w), y)
+    got = f64(y[at])
+    for e, i in rows.items():
+        v, err = F.product(thin[i], w[e])
+        near(got[i], v, F.rounded(v, err, "bf16"))
+    assert untouched(y, used)
+    # long rows in, and the weights' gradient of both
+    y[at] = dev(wide)
+    da = blank(L.rows, k)
+    mb.expert_bf16_dgrad(L.dims, L.bufs, n, k, y, dev(w), da)
+    dw = out(L.E, n, k, dtype="f32")
+    mb.expert_bf16_wgrad(L.dims, L.bufs, n, k, y, a, dw)
+    got = f64(da[at])
+    for e, i in rows.items():
+        v, err = F.row_grad(wide[i], w[e])
+        near(got[i], v, F.rounded(v, err, "bf16"))
+        v, err = F.weight_grad(wide[i], thin[i])
+        near(f64(dw[e]), v, F.rounded(v, err, "f32"))
+    assert untouched(da, used)
+    dw = out(L.E, k, n, dtype="f32")
+    mb.expert_bf16_wgrad(L.dims, L.bufs, k, n, a, y, dw)
+    for e, i in rows.items():
+        v, err = F.weight_grad(thin[i], wide[i])
+        near(f64(dw[e]), v, F.rounded(v, err, "f32"))
+
+
+@pytest.mark.parametrize("expected", [12, 3 << 17])
+def test_gated_rows_past_two_billion_elements(expected):
+    cap, n, k = 1 << 18, 1416, 72
+    L, used = region([[5], [0], [37]], cap, expected)
+    assert L.rows * 2 * n > 1 << 31
+    r = rng(expected, 1)
+    at = torch.from_numpy(used).to(G.dev())
+    x, w = bf(r, len(used), k), bf(r, L.E, 2 * n, k, std=k**-0.5)
+    a, y, pre = blank(L.rows, k), blank(L.rows, n), blank(L.rows, 2 * n)
+    a[at] = dev(x)
+    rows = {e: np.searchsorted(used, np.arange(lo, hi)) for e, lo, hi in L.groups}
+    mb.expert_bf16(L.dims, L.bufs, n, k, a, dev(w), y, act="swiglu", pre=pre)
+    got, gp = f64(y[at]), f64(pre[at])
+    for e, i in rows.items():
+        g, eg, u, eu, h, eh = F.gated(x[i], w[e])
+        near(got[i], h, F.rounded(h, eh, "bf16"))
+        near(gp[i], np.concatenate((g, u), 1), F.rounded(np.concatenate((g, u), 1),
+                                                         np.concatenate((eg, eu), 1), "bf16"))
+    assert untouched(y, used) and untouched(pre, used)
+    dp, w2 = blank(L.rows, 2 * n), bf(r, L.E, k, n, std=k**-0.5)
+    mb.expert_bf16_dgrad(L.dims, L.bufs, k, n, a, dev(w2), dp, act="swiglu", pre=pre)
+    got = f64(dp[at])
+    for e, i in rows.items():
+        dg, eg, du, eu = F.gate_grad(x[i], w2[e], gp[i, :n], gp[i, n:])
+        near(got[i, :n], dg, F.rounded(dg, eg, "bf16"))
+        near(got[i, n:], du, F.rounded(du, eu, "bf16"))
+    assert untouched(dp, used)
+
+
+@pytest.mark.parametrize("expected", [64, 64 * 40])
+def test_weights_past_two_billion_elements(expected):
+    """1024 experts; the first, one in the middle and the last have rows."""
+    n, k = 2064, 1032  # (half of n is a multiple of 8 too)
+    counts = np.zeros((64, 16), int)
+    counts[0, 0], counts[31, 5], counts[63, 15] = 3, 40, 21
+    r = rng(expected, 2)
+    some = [0, 31 * 16 + 5, 1023]
+    w = torch.full((1024, n, k), float("nan"), dtype=torch.bfloat16, device=G.dev())
+    assert w.numel() > 1 << 31
+    few = {e: bf(r, n, k, std=k**-0.5) for e in some}
+    for e in some:
+        w[e] = dev(few[e])
+    L = Layer(counts, 16, expected=expected)
+    a, dy = bf(r, L.rows, k), bf(r, L.rows, n)
+    y, da, mid = out(L.rows, n), out(L.rows, k), out(L.rows, n // 2)
+    mb.expert_bf16(L.dims, L.bufs, n, k, L.tensor(a), w, y)
+    mb.expert_bf16(L.dims, L.bufs, n // 2, k, L.tensor(a), w, mid, act="swiglu")
+    mb.expert_bf16_dgrad(L.dims, L.bufs, n, k, L.tensor(dy), w, da)
+    for e, lo, hi in L.groups:
+        v, err = F.product(a[lo:hi], few[e])
+        near(f64(y[lo:hi]), v, F.rounded(v, err, "bf16"))
+        _, _, _, _, v, err = F.gated(a[lo:hi], few[e])
+        near(f64(mid[lo:hi]), v, F.rounded(v, err, "bf16"))
+        v, err = F.row_grad(dy[lo:hi], few[e])
+        near(f64(da[lo:hi]), v, F.rounded(v, err, "bf16"))
+    del w
+    dw = blank(1024, n, k, dtype=torch.float32)
+    mb.expert_bf16_wgrad(L.dims, L.bufs, n, k, L.tensor(dy), L.tensor(a), dw)
+    rest = np.setdiff1d(np.arange(1024), some)
+    assert not any(bool(p.any()) for p in dw[torch.from_numpy(rest).to(G.dev())].split(64))
+    mb.expert_bf16_wgrad(L.dims, L.bufs, n, k, L.tensor(dy), L.tensor(a), dw, accumulate=True)
+    for e, lo, hi in L.groups:  # twice the sum, rounded in between
+        v, err = F.weight_grad(dy[lo:hi], a[lo:hi])
+        near(f64(dw[e]), 2 * v, 2 * F.rounded(v, err, "f32") + 2.0**-23 * np.abs(2 * v))
+
+
+@pytest.mark.parametrize("n,k,h", [
+    (300001, 1, 7168),     # both rows and tokens past 2^31 elements
+    ((1 << 22) + 7, 1, 8), ((1 << 21) + 3, 2, 1024), ((1 << 20) + 3, 1, 1032),  # the launch goes round
+])
+def test_combine_gradients_of_many_tokens(n, k, h):
+    g = torch.Generator(device=G.dev())
+    g.manual_seed(n)
+    d = mb.Dims.make(n, k, max(k, 2), 1, 0, h, cap=n * k + 3)
+    bufs = mb.PlanBuffers.allocate(d, G.dev())
+    bufs.pos = torch.randperm(n * k + 3, generator=g, device=G.dev())[: n * k].int().view(n, k)
+    bufs.status.zero_()
+    dy, ye = (torch.empty(m, h, dtype=torch.bfloat16, device=G.dev()).normal_(generator=g)
+              for m in (n, d.rows))
+    w = torch.rand(n, k, generator=g, device=G.dev())
+    go, gw = blank(d.rows, h), blank(n, k, dtype=torch.float32)
+    mb.combine_grad(d, bufs, dy, ye, w, go, gw)
+    for lo in range(0, n, 1 << 17):
+        t = slice(lo, min(lo + (1 << 17), n))
+        for j in range(k):
+            at = bufs.pos[t, j].long()
+            # one product in binary32, rounded once: the same bits
+            assert torch.equal(go[at], (w[t, j:j + 1] * dy[t].float()).bfloat16())
+            prod = dy[t].double() * ye[at].double()
+            err = (gw[t, j].double() - prod.sum(1)).abs()
+            bound = (h * F.ADD + F.STEP["f32"]) * prod.abs().sum(1) + F.TINY
+            assert bool((err <= bound).all())
+    rest = torch.ones(d.rows, dtype=torch.bool, device=G.dev())
+    rest[bufs.pos.view(-1).long()] = False
+    assert bool((go[rest] == torch.tensor(MARK, dtype=go.dtype, device=go.device)).all())
+
+
+@pytest.mark.parametrize("t,n,k,rank,L", [
+    ((1 << 19) + 600, 4104, 8, 8, 2), ((1 << 19) + 600, 8, 4104, 8, 2),  # outputs, rows
+    ((1 << 23) + 100, 8, 8, 256, 2),                                     # the inner sums
+    (5, 8200, 8, 256, 1024), (300, 8200, 8, 256, 1024),                  # the adapters
+    (5, 8, 8200, 256, 1024), (300, 264, 8200, 256, 1024),
+])
+def test_lora_past_two_billion_elements(t, n, k, rank, L):
+    g = torch.Generator(device=G.dev())
+    g.manual_seed(t + n)
+    r = rng(t, n)
+
+    def rows(m, c):
+        return torch.empty(m, c, dtype=torch.bfloat16, device=G.dev()).normal_(generator=g)
+
+    x, w, a, b = rows(t, k), rows(n, k), rows(L * rank, k), rows(L * n, rank)
+    assert max(t * n, t * k, t * rank, L * n * rank, L * rank * k) > 1 << 31
+    ad = np.sort(r.integers(-1, L, t))
+    ad[-1] = L - 1
+    prm = mb.LoraParams.make(t, n, k, rank, L)
+    y = blank(t, n)
+    mb.project_lora(prm, x, w, a.view(L, rank, k), b.view(L, n, rank),
+                    torch.ones(L, device=G.dev()), ints(ad), mb.alloc_lora_workspace(prm, G.dev()), y)
+    for i in np.unique(np.concatenate((np.arange(min(t, 5)), r.integers(0, t, 12), t - 1 - np.arange(5)))):
+        e = ad[i]
+        low = (f64(a[e * rank:(e + 1) * rank])[None], f64(b[e * n:(e + 1) * n])[None]) if e >= 0 else (
+            np.zeros((1, rank, k)), np.zeros((1, n, rank)))
+        want, err = F.lora(f64(x[i:i + 1]), f64(w), *low, np.ones(1), [0])
+        near(f64(y[i:i + 1]), want, F.rounded(want, err, "bf16"))
