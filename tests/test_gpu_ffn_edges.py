@@ -100,6 +100,48 @@ def test_wgrad_without_tokens_takes_no_rows_of_another_plan(add):
     assert marked(dw).all() if add else not f64(dw).any()
 
 
+def micros(call, calls=20):
+    """Time of a call among others, the least of some runs."""
+    best = float("inf")
+    for _ in range(6):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        for _ in range(calls):
+            call()
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b) * 1e3 / calls)
+    return best
+
+
+def test_empty_replica_slots_cost_little():
+    """1024 replica slots without rows, against none (20 us; the search of every
+    slot for every slot took 900)."""
+    n = k = 64
+    t = {}
+    for R in (0, 16):
+        L = Layer(np.pad(np.ones((64, 16), int), ((0, 0), (0, R))), 16)
+        dy, a, dw = out(L.rows, n), out(L.rows, k), out(L.E, n, k)
+        t[R] = micros(lambda: mb.expert_bf16_wgrad(L.dims, L.bufs, n, k, dy, a, dw))
+    assert t[16] < 5 * t[0], t
+
+
+def test_many_replicas_of_an_expert():
+    """Every replica slot holds one of two experts, and every second has rows."""
+    r = rng(21)
+    counts = np.ones((64, 18), int)
+    counts[:, 2:] = r.integers(0, 4, (64, 16)) * (np.arange(16) % 2)
+    L = Layer(counts, 2, r.integers(0, 2, (64, 16)) * 77 + 50, pad=1)
+    n, k = 40, 72
+    dy, a, dw = bf(r, L.rows, n), bf(r, L.rows, k), out(L.E, n, k, dtype="f32")
+    mb.expert_bf16_wgrad(L.dims, L.bufs, n, k, L.tensor(dy), L.tensor(a), dw)
+    got = f64(dw)
+    for e in range(L.E):
+        rows = np.concatenate([np.arange(lo, hi) for x, lo, hi in L.groups if x == e])
+        v, err = F.weight_grad(dy[rows], a[rows])
+        near(got[e], v, F.rounded(v, err, "f32"))
+
+
 # ------------------------------------------------------------ far gates
 
 @pytest.mark.parametrize("rows", [3, 64, 300])

@@ -304,9 +304,14 @@ __device__ __forceinline__ int slot_at(const SlotTable& s, int nslots, int t, in
 }
 
 // The lists of the plan: an expert's home slot, then its replicas in
-// ascending order.
+// ascending order. One wave links the replica slots, 64 at a time from the
+// last to the first: a lane's next is the first behind it that holds the same
+// expert, found by one ballot for every bit of its number, else the head of
+// the expert's list so far. (1024 of them: 4 us of the call. A search of the
+// slots behind each took 900.)
 template <class Args>
 __device__ void expert_lists(const Args& p, int nslots, ExpertLists& t) {
+  static_assert(kMaxExperts == 1 << 10, "the bits of an expert's number");
   for (int j = threadIdx.x; j < nslots; j += kExpertThreads) {
     int lo, hi, e;
     slot_rows(p, j, lo, hi, e);
@@ -314,38 +319,33 @@ __device__ void expert_lists(const Args& p, int nslots, ExpertLists& t) {
     t.n[j] = hi - lo;
     t.next[j] = hi > lo ? e : -1;  // its expert, for now
   }
+  for (int e = threadIdx.x; e < p.E; e += kExpertThreads) t.first[e] = -1;
   __syncthreads();
-  // the first replica slot of e from the q-th on
-  auto replica = [&](int e, int q) {
-    for (; q < p.P * p.R; ++q) {
-      const int s = q / p.R * p.NS + p.Eh + q % p.R;
-      if (t.next[s] == e) return s;
+  if (threadIdx.x < 64) {
+    const int lane = threadIdx.x, replicas = p.P * p.R;
+    auto slot = [&](int q) { return q / p.R * p.NS + p.Eh + q % p.R; };
+    for (int q = (replicas - 1) & ~63; q >= 0; q -= 64) {
+      const bool in = q + lane < replicas;
+      const int s = in ? slot(q + lane) : 0, e = in ? t.next[s] : -1;
+      uint64_t same = __ballot(e >= 0);
+#pragma unroll
+      for (int b = 0; b < 10; ++b) {
+        const uint64_t set = __ballot(e >> b & 1);
+        same &= e >> b & 1 ? set : ~set;
+      }
+      if (e >= 0) {
+        const uint64_t behind = same & (~1ull << lane);
+        t.next[s] = behind ? slot(q + __builtin_ctzll(behind)) : t.first[e];
+        if (lane == __builtin_ctzll(same)) t.first[e] = s;
+      }
+      __builtin_amdgcn_wave_barrier();  // the next 64 read the heads after these wrote them
     }
-    return -1;
-  };
-  constexpr int kEach = kMaxPlanSlots / kExpertThreads;
-  int next[kEach];
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int j = threadIdx.x + i * kExpertThreads;
-    next[i] = -1;
-    if (j >= nslots) continue;
-    const int rank = j / p.NS, at = j - rank * p.NS;
-    if (at < p.Eh)
-      next[i] = replica(rank * p.Eh + at, 0);
-    else if (t.next[j] >= 0)
-      next[i] = replica(t.next[j], rank * p.R + at - p.Eh + 1);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int j = threadIdx.x + i * kExpertThreads;
-    if (j < nslots) t.next[j] = next[i];
   }
   __syncthreads();
   for (int e = threadIdx.x; e < p.E; e += kExpertThreads) {
     const int rank = e / p.Eh, home = rank * p.NS + e - rank * p.Eh;
-    const int first = t.n[home] ? home : t.next[home];
+    t.next[home] = t.first[e];
+    const int first = t.n[home] ? home : t.first[e];
     int s = 0;
     for (int j = first; j >= 0; j = t.next[j]) s += (t.n[j] + 63) / 64;
     t.first[e] = first;
