@@ -126,6 +126,21 @@ def test_empty_replica_slots_cost_little():
     assert t[16] < 5 * t[0], t
 
 
+@pytest.mark.parametrize("t,n", [(4000, 8), (1000, 64), (240, 256)])
+def test_lora_narrow_outputs_use_the_whole_gpu(t, n):
+    """As many 16 x 16 tiles as CUs take little more than one (1.3 to 2.1 times;
+    a workgroup to a column alone took 10 to 140)."""
+    k, r = 7168, rng(t)
+    took = {}
+    for rows, cols in ((16, 16), (t, n)):
+        prm = mb.LoraParams.make(rows, cols, k, 16, 2)
+        x, w, a, b, y = out(rows, k), out(cols, k), out(2, 16, k), out(2, cols, 16), out(rows, cols)
+        args = (x, w, a, b, torch.ones(2, device=G.dev()), ints(r.integers(0, 2, rows)),
+                mb.alloc_lora_workspace(prm, G.dev()), y)
+        took[rows] = micros(lambda: mb.project_lora(prm, *args))
+    assert took[t] < 6 * took[16], took
+
+
 def test_many_replicas_of_an_expert():
     """Every replica slot holds one of two experts, and every second has rows."""
     r = rng(21)

@@ -165,9 +165,12 @@ Shape shape_of(const mb_lora_params& p) {
   const int blocks = (p.n_rows + 15) / 16, turns = (p.k_in + 4 * kDownStep - 1) / (4 * kDownStep);
   s.down_parts = blocks >= 64 ? 1 : std::min(turns, 4);
   s.v = (size_t)s.down_parts * p.n_rows * p.rank;
-  // 16 rows, n_out = k_in = 4096: 19 us (tiles: 25); 24 rows: 28 (27). Small
-  // products leave CUs idle in tiles (32 rows, 1024: 16 us, tiles 20).
-  s.few = p.n_rows <= 16 || (int64_t)blocks * ((p.n_out + 15) / 16) < kCus;
+  // A block of rows, or no more than a 16 x 16 tile to a CU, straight from
+  // memory, us, against the tiles: 16 rows, n_out = k_in = 4096 19, 25 (24
+  // rows: 28, 27); k_in = 7168: 240 rows, n_out = 256 28, 34; 4000 rows, 8 42,
+  // 51; 64 rows, 1024 23, 31. Two tiles to a CU (64 rows, 2048): 37, 31, though of
+  // short reductions they are the faster too (k_in = 1024: 11, 21).
+  s.few = p.n_rows <= 16 || (int64_t)blocks * ((p.n_out + 15) / 16) <= kCus;
   // else the cheapest of both tiles and of up to as many parts as the CUs take
   // at once, of at least four stages. n_out = k_in = 7168, the best of 128-row
   // tiles against 256-row tiles, us: 384 rows 74, 85; 1024 rows 123, 151;
@@ -222,7 +225,8 @@ hipError_t launch_project_lora(const mb_lora_params& q, const uint16_t* x, const
   const bool bf16 = q.dtype_out == MB_BF16;
   const dim3 cus(kCus);
   if (s.few) {
-    const dim3 grid(std::min((q.n_out + 15) / 16, kFewGroups)), wide(512);
+    const dim3 grid((unsigned)std::min<int64_t>((int64_t)blocks * ((q.n_out + 15) / 16), kFewGroups));
+    const dim3 wide(512);
     if (bf16)
       hipLaunchKernelGGL((k_bf16_few<kTileLora, true, 8, 8>), grid, wide, 0, st, p);
     else
