@@ -13,7 +13,8 @@ import token_dispatch_mb_amd as mb
 from . import gpu_harness as G
 from . import plain_ffn as F
 from . import plain_ops as R
-from .test_gpu_ffn import MARK, Layer, bf, dev, f64, marked, near, out, rng
+from .test_gpu_ffn import (LAYERS, MARK, SIZES, Layer, Step, bf, dev, f64, marked, near, out, rng,
+                           run_product)
 
 pytestmark = pytest.mark.gpu
 
@@ -24,6 +25,9 @@ def _gpu_required():
         pytest.skip("needs a GPU")
     yield
     torch.cuda.synchronize()
+
+
+TILES = 1 << 17  # rows expected that make any product take the tiles
 
 
 def ints(a):
@@ -157,17 +161,104 @@ def test_many_replicas_of_an_expert():
         near(got[e], v, F.rounded(v, err, "f32"))
 
 
+# ------------------------------------------------------------ tiles, and few rows
+
+@pytest.mark.parametrize("n,k", SIZES)
+@pytest.mark.parametrize("layer", [name for name in LAYERS if name != "few"])
+def test_products_in_tiles(layer, n, k):
+    """Sizes that by themselves would take their operands straight from memory."""
+    run_product(LAYERS[layer](expected=TILES), n, k, "none", "bf16")
+    run_product(LAYERS[layer](expected=TILES, dtype_out="f32"), n, k, "none", "f32")
+    run_product(LAYERS[layer](expected=TILES), n, k, "swiglu", "bf16")
+    run_product(LAYERS[layer](expected=TILES), n, k, "swiglu", "bf16", keep=False)
+
+
+@pytest.mark.parametrize("counts,home", [
+    ([[9]], 1), ([[16]], 1), ([[17]], 1), ([[64]], 1), ([[129]], 1),
+    ([[12], [0], [33], [5]], 1), ([[16, 16, 16, 16]], 4), ([[1, 140, 0, 3]], 3),
+])
+def test_products_of_few_rows_and_slots(counts, home):
+    """On both sides of where the columns of tiles leave more than half the CUs
+    idle: outputs of one column up to 130."""
+    for n, k in ((264, 520), (4104, 264), (16648, 40)):
+        run_product(Layer(counts, home, pad=1), n, k, "none", "bf16")
+        run_product(Layer(counts, home, dtype_out="f32"), n, k, "none", "f32")
+        run_product(Layer(counts, home), n, k, "swiglu", "bf16")
+
+
+@pytest.mark.parametrize("expected", [2, TILES])
+def test_infinities_stay_in_their_rows_and_columns(expected):
+    L = Layer([[40, 3]], 2, expected=expected, dtype_out="f32")
+    n, k = 24, 88
+    r = rng(5, expected)
+    a, w = bf(r, L.rows, k), bf(r, 2, n, k)
+    a[7, 80], w[0, 5, 3], a[41, 0] = np.nan, np.inf, -np.inf
+    y = out(L.rows, n, dtype="f32")
+    mb.expert_bf16(L.dims, L.bufs, n, k, dev(a), dev(w), y)
+    want = np.ones((L.rows, n), bool)
+    want[7], want[:40, 5], want[41] = False, False, False
+    assert np.array_equal(np.isfinite(f64(y)), want)
+
+
+@pytest.mark.parametrize("expected", [2, TILES])
+def test_products_under_a_fatal_status(expected):
+    L = Layer([[37, 0, 5, 1], [0, 70, 13, 2]], 3, expected=expected)
+    L.bufs.status[0] = mb.ST_CAPACITY
+    y, pre = out(L.rows, 64), out(L.rows, 128)
+    a, w = out(L.rows, 72), out(L.E, 128, 72)
+    mb.expert_bf16(L.dims, L.bufs, 64, 72, a, w, y)
+    mb.expert_bf16(L.dims, L.bufs, 64, 72, a, w, y, act="swiglu", pre=pre)
+    assert marked(y).all() and marked(pre).all()
+
+
+def test_a_slot_of_few_rows_takes_little_more_than_eight():
+    """Nine rows in one slot are as many 16-row blocks as eight (1.0 times; in
+    tiles, which leave nine CUs of ten idle, 3.2)."""
+    h, i = 7168, 3200
+    w, took = out(1, 2 * i, h), {}
+    for rows in (8, 9, 16):
+        L = Layer([[rows]], 1)
+        a, y = out(rows, h), out(rows, i)
+        took[rows] = micros(lambda: mb.expert_bf16(L.dims, L.bufs, i, h, a, w, y, act="swiglu"))
+    assert max(took.values()) < 2 * took[8], took
+
+
+def test_a_training_step_in_tiles():
+    """As a_training_step, whose bounds these are, with rows enough for tiles in
+    every product, captured and replayed."""
+    s = Step(N=3000, H=1032, I=520, seed=9)
+    s.run()
+    for name, want in s.exact().items():
+        want, got = want.detach().numpy(), f64(s.o[name])
+        rms = np.sqrt((want**2).mean())
+        near(got, want, 12 * 2.0**-8 * (rms + np.abs(want)))
+    keep = {k: s.o[k].clone() for k in ("y", "dx", "dgate", "dw1", "dw2")}
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        s.run(st)
+    for _ in range(3):
+        for v in s.o.values():
+            v.fill_(MARK)
+        g.replay()
+        torch.cuda.synchronize()
+        for k, v in keep.items():
+            assert torch.equal(s.o[k], v), k
+
+
 # ------------------------------------------------------------ far gates
 
+@pytest.mark.parametrize("expected", [1, TILES])
 @pytest.mark.parametrize("rows", [3, 64, 300])
-def test_far_gates_of_large_ups_keep_their_value(rows):
+def test_far_gates_of_large_ups_keep_their_value(rows, expected):
     """silu(g) u where silu(g) alone is below binary32 and u brings it back."""
     gates = np.array([-170, -150, -130, -110, -104, -95, -88.5, -81, -60, -3, 0.5, 90])
     ups = 2.0 ** np.array([0, 30, 60, 90, 120])
     n, k = len(gates) * len(ups) + 4, 8
     pair = np.array([(g, u) for g in gates for u in ups] + [(1, 1)] * 4)
     pair = R.bf16_round(np.float32(pair)).astype(np.float64)
-    L = Layer([[rows]], 1)
+    L = Layer([[rows]], 1, expected=expected)
     a = np.zeros((rows, k))
     a[:, 0] = 1
     w = np.zeros((1, 2 * n, k))
@@ -273,7 +364,7 @@ def test_gated_rows_past_two_billion_elements(expected):
     assert untouched(dp, used)
 
 
-@pytest.mark.parametrize("expected", [64, 64 * 40])
+@pytest.mark.parametrize("expected", [64, TILES])
 def test_weights_past_two_billion_elements(expected):
     """1024 experts; the first, one in the middle and the last have rows."""
     n, k = 2064, 1032  # (half of n is a multiple of 8 too)

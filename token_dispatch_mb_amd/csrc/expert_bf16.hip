@@ -35,9 +35,22 @@ bool long_tiles(int64_t tiles256, int64_t tiles128) {
 // From the rows expected in a slot, and 32 more, half of the 64 that tiles leave
 // out of a slot's last one at a time.
 //
-// Few rows: 64 slots, the products of 4096 x 2048 and back: 256 rows 531 us,
-// in tiles 630; 512 rows 645 and 675; 1024 rows 965 and 765.
-// 128 and 256 rows to a tile, the same: 4096 rows 706 and 715 us, 8192 rows
+// Few rows, straight from memory: up to eight in a slot, or where the columns
+// of tiles, times the 16-row blocks that would each pass the weights, are fewer
+// than half the CUs, since tiles leave the rest idle. us, against tiles:
+//   7168 -> 2 x 3200 and back (25 and 28 columns): 1 slot, 9 rows 25 + 15, 79 +
+//     41; 32 rows 43 + 27, 79 + 42; 64 rows 79 + 44, 80 + 42. 4 slots, 9 rows 94
+//     + 37, 109 + 47; 24 rows 147 + 76, 110 + 47. 8 slots, 8 rows 164 + 83, 130
+//     + 67 (the rule misses this one); 9 rows 166 + 86, 130 + 67.
+//   4096 -> 2 x 2048 and back (16 and 16): 1 slot, 64 rows 27 + 19, 45 + 24; 128
+//     rows 48 + 33, 51 + 28. 8 slots, 24 rows 91 + 56, 64 + 33. 64 slots, 4 rows
+//     387 + 202, 547 + 230; 8 rows 410 + 230, 551 + 231; 16 rows 467 + 279, 552 +
+//     232.
+//   8192 -> 2048 (8): 1 slot, 128 rows 61, 83; 256 rows 118, 86. 7168 -> 256 (1): 1
+//     slot, 1024 rows 55, 75; 1700 rows 92, 76 (missed).
+// The rows' gradients have tiles only, which few slots leave idle too: 7168 x
+// 3200, 1 slot 66 and 77 us at 4 as at 64 rows, 8 slots 106 and 129.
+// 128 and 256 rows to a tile, 64 slots: 4096 rows 706 and 715 us, 8192 rows
 // 795 and 768, 32768 rows 1830 and 1617; one slot, 7168 x 4096 and back: 1024
 // rows 180 and 277, 2048 rows 326 and 290, 4096 rows 627 and 562.
 template <int kMode, bool kBF16>
@@ -47,7 +60,8 @@ void launch_tiles(const TileArgs& p, int64_t rows, hipStream_t st) {
   const int64_t columns = (p.n + across - 1) / across;
   const dim3 grid(kCus), block(kExpertThreads);
   if constexpr (kMode == kTileProduct || kMode == kTileGated) {
-    if (rows <= slots * 8) {
+    const int64_t blocks = (rows + slots * 16 - 1) / (slots * 16) * slots;
+    if (rows <= slots * 8 || blocks * columns < kCus / 2) {
       hipLaunchKernelGGL((k_bf16_few<kMode, kBF16, 4, 4>), dim3(kFewGroups), block, 0, st, p);
       return;
     }
