@@ -194,17 +194,17 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
     ra = buffer_of(p.a + (size_t)next.m0 * kb, (uint32_t)na * kb);
     ras = buffer_of(p.a_scale + (size_t)next.m0 * ks, (uint32_t)na * ks);
   };
-  // Copy c of a pair's rows: 8 of weights, then 2 JT. With an odd number of
-  // steps the second half of the last pair lies behind the row: its lanes
-  // read out of range, zeros.
-  auto copy_w = [&](int pair, int c) {
+  // Copy c of a pair's rows: 8 of weights, then 2 JT, from a buffer that is
+  // settled for all of them. With an odd number of steps the second half of
+  // the last pair lies behind the row: its lanes read out of range, zeros.
+  auto copy_w = [&](i32x4 rows, int pair, int c) {
     const uint32_t last = 2 * pair + 1 == steps ? 0x80000000u : 0u;
-    copy16(rw, (lds_ptr)(lds.w[c_buf] + (wave * 8 + c) * 1024),
+    copy16<0>(rows, (lds_ptr)(lds.w[c_buf] + (wave * 8 + c) * 1024),
            (cw[c & 1] + (wave * 8 + c) * 8 * kb) | (cut_w & last), pair * 128);
   };
-  auto copy_a = [&](int pair, int c) {
+  auto copy_a = [&](i32x4 rows, int pair, int c) {
     const uint32_t last = 2 * pair + 1 == steps ? 0x80000000u : 0u;
-    copy16(ra, (lds_ptr)(lds.a[c_buf] + (wave * 2 * JT + c) * 1024),
+    copy16<0>(rows, (lds_ptr)(lds.a[c_buf] + (wave * 2 * JT + c) * 1024),
            (ca[c & 1] + (wave * 2 * JT + c) * 8 * kb) | (cut_a[c & 1] & last), pair * 128);
   };
   // The scales of a pair and the next; nothing in the second pair of a group.
@@ -248,10 +248,11 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
   aim(0);
 #pragma unroll
   for (int pair = 0; pair < 2; ++pair) {
+    const i32x4 w = settled(rw), a = settled(ra);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) copy_w(pair, c);
+    for (int c = 0; c < 8; ++c) copy_w(w, pair, c);
 #pragma unroll
-    for (int c = 0; c < 2 * JT; ++c) copy_a(pair, c);
+    for (int c = 0; c < 2 * JT; ++c) copy_a(a, pair, c);
     c_buf ^= 1;
   }
   late_ws = rws, late_as = ras;
@@ -292,6 +293,8 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const uint8_t* as = e && behind ? lds.none : lds.as[grp];
+        i32x4 w, a;
+        if (e) w = settled(rw);
         // first half: the rows of the second are read under it
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
@@ -301,7 +304,7 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
             acc[i][j] = mfma_mx4(fw[i][u], fa[j][u], acc[i][j], sw[i], sa[j], u);
           if (!kHalf && c < JT) read_a(buf, e, JH + (c >> 1), c & 1);
           if (!kHalf && c < JH) sa[JH + c] = scales(as, (2 * (JH + c) + hm) * 32 + r, gs + e);
-          if (e) copy_w(ahead, c);
+          if (e) copy_w(w, ahead, c);
           if (!e && c < 2) copy_scales(c);
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -316,6 +319,7 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
         const int ns = e ? (s + 1 == pairs ? 0 : (gs + 2) & 2) : gs + 1;  // the next step in its group
         const uint8_t* nas = !e && behind ? lds.none : lds.as[grp];
         const uint8_t* nws = !e && behind ? lds.none : lds.ws[grp];
+        if (e) a = settled(ra);
         // second half: the next step's operands are read under it, and the
         // pair two ahead copied into the buffer just read
 #pragma unroll
@@ -330,7 +334,7 @@ __global__ __launch_bounds__(kExpertThreads, 1) void k_expert_tile(ExpertArgs p)
           if (c < JH) sa[c] = scales(nas, (2 * c + hm) * 32 + r, ns);
           if (e) {
 #pragma unroll
-            for (int d = c * JT / 4; d < (c + 1) * JT / 4; ++d) copy_a(ahead, d);
+            for (int d = c * JT / 4; d < (c + 1) * JT / 4; ++d) copy_a(a, ahead, d);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
