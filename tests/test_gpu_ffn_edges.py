@@ -91,6 +91,22 @@ def test_lora_infinities_keep_their_sign(t, n, k, order):
     near(got[good], want[good], F.rounded(want, err, "f32")[good])
 
 
+@pytest.mark.parametrize("t,n,k", [(16, 72, 72), (64, 1032, 1032), (300, 520, 136)])
+def test_lora_vanishing_inner_sums(t, n, k):
+    """Inner sums down to the smallest binary32 numbers and below."""
+    r = rng(t, n, 12)
+    x, w = bf(r, t, k), bf(r, n, k)
+    a, b = np.zeros((3, 8, k)), bf(r, 3, n, 8)
+    a[:, np.arange(8), np.arange(8)] = 1
+    scale, ad = 2.0 ** np.array([-100, -126, -146]), np.arange(t) % 4 - 1
+    prm = mb.LoraParams.make(t, n, k, 8, 3, dtype_out="f32")
+    y = out(t, n, dtype="f32")
+    mb.project_lora(prm, dev(x), dev(w), dev(a), dev(b), dev(scale, torch.float32), ints(ad),
+                    mb.alloc_lora_workspace(prm, G.dev()), y)
+    want, err = F.lora(x, w, a, b, scale, ad)
+    near(f64(y), want, F.rounded(want, err, "f32"))
+
+
 # ------------------------------------------------------------ weights' gradients
 
 @pytest.mark.parametrize("add", [False, True])
