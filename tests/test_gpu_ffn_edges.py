@@ -476,3 +476,64 @@ def test_lora_past_two_billion_elements(t, n, k, rank, L):
             np.zeros((1, rank, k)), np.zeros((1, n, rank)))
         want, err = F.lora(f64(x[i:i + 1]), f64(w), *low, np.ones(1), [0])
         near(f64(y[i:i + 1]), want, F.rounded(want, err, "bf16"))
+
+
+@pytest.mark.parametrize("expected", [1, TILES])
+def test_the_widest_outputs_and_longest_sums(expected):
+    """2^20 outputs, and sums of 2^20 terms, of one slot with a tile and a rest."""
+    wide, k, rows = 1 << 20, 8, 70
+    L = Layer([[rows]], 1, pad=1, expected=expected, dtype_out="f32")
+    r = rng(expected, 7)
+    a, w = bf(r, L.rows, k), bf(r, 1, wide, k)
+    y = out(L.rows, wide, dtype="f32")
+    mb.expert_bf16(L.dims, L.bufs, wide, k, L.tensor(a), dev(w), y)
+    v, err = F.product(a[:rows], w[0])
+    near(f64(y[:rows]), v, F.rounded(v, err, "f32"))
+    assert marked(y[rows:]).all()
+    half = wide // 2
+    mid, pre = out(L.rows, half), out(L.rows, wide)
+    mb.expert_bf16(L.dims, L.bufs, half, k, L.tensor(a), dev(w), mid, act="swiglu", pre=pre)
+    g, eg, u, eu, h, eh = F.gated(a[:rows], w[0])
+    near(f64(mid[:rows]), h, F.rounded(h, eh, "bf16"))
+    near(f64(pre[:rows, :half]), g, F.rounded(g, eg, "bf16"))
+    near(f64(pre[:rows, half:]), u, F.rounded(u, eu, "bf16"))
+    # the gradient of the rows: sums of 2^20 terms, then 2^20 of them
+    dy = bf(r, L.rows, wide, std=2.0**-10)
+    da = out(L.rows, k, dtype="f32")
+    mb.expert_bf16_dgrad(L.dims, L.bufs, wide, k, L.tensor(dy), dev(w), da)
+    v, err = F.row_grad(dy[:rows], w[0])
+    near(f64(da[:rows]), v, F.rounded(v, err, "f32"))
+    w2, p = bf(r, 1, k, half), f64(pre)[:rows]
+    dp = out(L.rows, wide)
+    mb.expert_bf16_dgrad(L.dims, L.bufs, k, half, L.tensor(a), dev(w2), dp, act="swiglu", pre=pre)
+    dg, eg, du, eu = F.gate_grad(a[:rows], w2[0], p[:, :half], p[:, half:])
+    near(f64(dp[:rows, :half]), dg, F.rounded(dg, eg, "bf16"))
+    near(f64(dp[:rows, half:]), du, F.rounded(du, eu, "bf16"))
+    for one, two in ((dy, a), (a, dy)):
+        dw = out(1, one.shape[1], two.shape[1], dtype="f32")
+        mb.expert_bf16_wgrad(L.dims, L.bufs, one.shape[1], two.shape[1], L.tensor(one), L.tensor(two), dw)
+        v, err = F.weight_grad(one[:rows], two[:rows])
+        near(f64(dw[0]), v, F.rounded(v, err, "f32"))
+
+
+@pytest.mark.parametrize("t,n,k", [(5, 1 << 20, 8), (70, 1 << 20, 8), (5, 8, 1 << 20), (70, 8, 1 << 20),
+                                   (300, 264, 1 << 18), (1 << 26, 8, 8)])
+def test_lora_of_the_largest_sizes(t, n, k):
+    g = torch.Generator(device=G.dev())
+    g.manual_seed(t + n)
+
+    def rows(m, c, std=1.0):
+        return torch.empty(m, c, dtype=torch.bfloat16, device=G.dev()).normal_(0, std, generator=g)
+
+    x, w, a, b = rows(t, k), rows(n, k, k**-0.5), rows(16, k, k**-0.5), rows(2 * n, 8)
+    ad = torch.randint(-1, 2, (t,), generator=g, device=G.dev(), dtype=torch.int32)
+    prm = mb.LoraParams.make(t, n, k, 8, 2, dtype_out="f32")
+    y = blank(t, n, dtype=torch.float32)
+    mb.project_lora(prm, x, w, a.view(2, 8, k), b.view(2, n, 8), torch.ones(2, device=G.dev()), ad,
+                    mb.alloc_lora_workspace(prm, G.dev()), y)
+    some = np.unique(np.concatenate((np.arange(min(t, 9)), t - 1 - np.arange(5), rng(t).integers(0, t, 9))))
+    at = torch.from_numpy(some).to(G.dev())
+    want, err = F.lora(f64(x[at]), f64(w), f64(a).reshape(2, 8, k), f64(b).reshape(2, n, 8), np.ones(2),
+                       ad[at].tolist())
+    near(f64(y[at]), want, F.rounded(want, err, "f32"))
+    assert bool((y != MARK).any(1).all())
