@@ -19,8 +19,8 @@
  * mb_expert_mx4 multiplies the dispatched 4-bit rows by their experts'
  * weights. mb_expert_bf16 does so from bf16 rows and weights, as the two halves
  * of a gated feed-forward block; its gradients and the combine's train such a
- * layer. mb_project_lora serves the projections around the experts with the
- * low-rank adapters of many requests.
+ * layer. mb_project_lora is a dense projection with the low-rank adapters of
+ * many requests, for a program's other layers: it takes no plan.
  *
  * The P logical ranks of the expert-parallel group are partitions of one
  * GPU's memory: rank r owns rows [r*cap, (r+1)*cap) of every [P*cap, ...]
@@ -626,16 +626,16 @@ typedef struct mb_lora_params {
 size_t mb_lora_workspace_bytes(const mb_lora_params* prm);
 
 /*
- * A projection that all requests share, and beside it the low-rank adapter of
- * each request (the projections around the experts: attention's, the shared
- * expert's), a = adapter[t]:
+ * A projection that all requests share (one of a program's own beside the
+ * experts: attention's, a shared expert's), and the low-rank adapter of each
+ * request, a = adapter[t]:
  *   y[t][j] = sum_i x[t][i] * w[j][i]
  *           + sum_q (scale[a] * sum_i x[t][i] * lora_a[a][q][i]) * lora_b[a][j][q],
  * the second line only where a is in [0, L): rows with any other number have no
  * adapter. Accumulated in fp32, the inner sums not rounded in between, and
  * rounded once (to nearest even). Rows of one adapter need not be consecutive,
  * though a run of them costs less (4096 rows of 64 adapters in turn, 4096 x
- * 4096: 1.9 ms, in runs 0.18). What is not finite in an adapter stays in the
+ * 4096: 0.44 ms at rank 16, 0.94 at 64; in runs 0.14 and 0.18). What is not finite in an adapter stays in the
  * rows that have it, and gives what the formula does: an infinite element of
  * lora_b is one times any inner sum but 0 (of sums below 2^-94 some may count
  * as 0).

@@ -36,14 +36,19 @@
 // gradient, 1.14 in the weights' (a library product reaches 1.60, 1.39 and
 // 1.21 on the same operands). A stage takes 2420 cycles, 2048 of them
 // products: what a wave issues between two products goes past their 32
-// cycles here and there, and power holds the clock below its peak. A tile
-// costs 17 to 20 thousand more, half of them stores, which the next tile's
-// first stage covers in part; slots whose rows are no multiple of 256 and
-// reductions of 2048 and 4096 elements therefore run at 0.95 to 1.05.
+// cycles here and there, and power holds the clock at 1.4 to 1.9 GHz in calls
+// of a millisecond and more. A tile costs 17 to 20 thousand cycles more, half
+// of them stores, which the next tile's first stage covers in part; slots
+// whose rows are no multiple of 256 and reductions of 2048 and 4096 elements
+// therefore run at 0.95 to 1.05. Tiles are whole to a workgroup: 600 of them
+// on 256 CUs take three rounds, in which a CU is busy 70 % of the time (8192
+// rows of 8 experts, 4096 outputs: 0.85 to 0.95). LDS has no bank conflicts.
 // Four waves hold 256 accumulators each and all of the vector registers, so
-// there is one to a SIMD: eight waves of half the tile would read LDS twice as
-// much for each product. Row tiles walked together (kGroupM) 1, 2, 4 or 8:
-// within 2 %.
+// there is one to a SIMD. Eight waves of 128 x 64 would read LDS 1.5 times as
+// much for each product, within what it can deliver; they were not built. Row
+// tiles walked together (kGroupM) 1, 2, 4 or 8: within 2 %. The gates'
+// gradient spills 48 vector registers at 256 rows, between tiles and around
+// their stores, the adapters' product about 200, in its part after the stages.
 //
 // What lies outside an operand is read as zeros, by the length in the buffer
 // descriptor: rows and reduction rows past the end, pieces past the end of a
@@ -366,8 +371,9 @@ __device__ void expert_lists(const Args& p, int nslots, ExpertLists& t) {
 
 // ---- few rows: operands straight from memory --------------------------------
 //
-// The columns' operand is read once, and sets the pace: 128 rows over 80 slots,
-// 7168 -> 2 x 2048 and back, in 0.79 to 0.87 ms, 6.5 to 7.1 TB/s of weights. A
+// The columns' operand is read once for every slot, and sets the pace: 128 rows
+// over 80 slots, 58 of them with rows, 7168 -> 2 x 2048 and back, in 0.62 and
+// 0.30 ms, 5.5 and 5.7 TB/s of weights (a contiguous read here: 6.7). A
 // workgroup computes 16 outputs of 16 rows, whatever a slot holds of them; its
 // waves take 32 U elements of the reduction at a time by turns, so that a
 // weight row is read in whole lines by waves that follow each other, and add up

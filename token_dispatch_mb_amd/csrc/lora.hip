@@ -5,8 +5,11 @@
 //
 // k_lora_down makes v, in binary32; the product then goes on over the ranks
 // of the adapters among a tile's rows, so that w and y are passed once. 16384
-// rows, 7168 x 7168, rank 32: 0.08 and 1.35 ms, 1.19 PFLOP/s in all (without any
-// adapter the same: the matrix unit's power and the tiles' ends bound it). 64
+// rows, 7168 x 7168, rank 32: 0.09 to 0.11 and 1.35 to 1.4 ms, 1.17 PFLOP/s in
+// all (without any adapter the same: the matrix unit's power and the tiles' ends
+// bound it). Rows whose adapters differ within 32 rows compute one after the
+// other, each waiting for its own loads: 4096 rows of 64 adapters in turn, 4096 x
+// 4096, rank 16 0.44 ms, in runs 0.14. 64
 // rows with an adapter each: 8, 23 and 9 us for v, the product in nine parts
 // (4.4 TB/s of w) and their sum, bound by the latency of three short kernels.
 #include <algorithm>

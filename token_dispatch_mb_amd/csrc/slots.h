@@ -111,7 +111,8 @@ __device__ __forceinline__ i32x4 buffer_of(const void* p, uint32_t bytes) {
 // The compiler does not look into the assembly for hazards: a scalar register
 // that a vector instruction wrote (a lane read back, of a value or of a
 // spilled register) is valid for memory instructions five wait states later.
-// kNops waits that long before the copy.
+// kNops waits that long before the copy (one now and then; where there are
+// many, their buffer waits for all of them, see settled).
 template <int kNops = 4>
 __device__ __forceinline__ void copy16(i32x4 buf, lds_ptr to, uint32_t voff, uint32_t soff) {
   asm volatile("s_nop %4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
